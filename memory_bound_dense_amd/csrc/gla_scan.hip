@@ -1,0 +1,467 @@
+// libgemv.so, continued: gated linear attention over whole sequences
+// (include/gla_scan.h) over the kernels of gla_scan_kernel.h.
+#include "gla_scan.h"
+
+#include "gla_scan_kernel.h"
+#include "gla_scan_table.h"
+#include "handle.h"
+#include "operand.h"
+
+namespace mbd {
+
+// ---- segments' states from their own states ----------------------------------
+// slots[s] holds segment s's own state (from zero) and becomes its start
+// state: one thread per 4 elements walks the sequence's segments.
+struct JoinArgs {
+  float* slots;
+  const float* sums;
+  const float* S0;          // user layout, or null
+  const int32_t* offsets;
+  int64_t total, t;
+  int32_t H, dk, dv, dkp, dvp, nseg, L, rev;
+};
+__global__ __launch_bounds__(256) void scan_join_kernel(const JoinArgs a) {
+  const int per = a.dkp * (a.dvp / 4), nx = (per + 255) / 256;
+  const int64_t head = blockIdx.x / nx;            // seq * H + h
+  const int seq = (int)(head / a.H);
+  const int i = (int)(blockIdx.x - head * nx) * 256 + threadIdx.x;
+  if (i >= per) return;
+  int64_t len = a.t;
+  if (a.offsets) {
+    const int64_t s = min(max((int64_t)a.offsets[seq], (int64_t)0), a.total);
+    len = min(min(max((int64_t)a.offsets[seq + 1], s), a.total) - s, a.t);
+  }
+  const int ns = max((int)((len + a.L - 1) / a.L), 1);
+  const int d = i / (a.dvp / 4), e = (i - d * (a.dvp / 4)) * 4;
+  f32x4 x = {};
+  if (a.S0 && d < a.dk) {
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+      if (e + r < a.dv) x[r] = a.S0[(head * a.dk + d) * a.dv + e + r];
+  }
+  const int64_t size = (int64_t)a.dkp * a.dvp;
+  float* slot = a.slots + head * a.nseg * size + (int64_t)d * a.dvp + e;
+  const float* sum = a.sums + head * a.nseg * a.dkp + d;
+#pragma unroll 4
+  for (int s = 0; s < ns; ++s) {
+    const int64_t at = a.rev ? ns - 1 - s : s;
+    f32x4* to = (f32x4*)(slot + at * size);
+    const f32x4 u = *to;
+    const float f = expf(sum[at * a.dkp]);
+    *to = x;
+    x = x * f + u;
+  }
+}
+
+}  // namespace mbd
+
+using mbd_host::kMagic;
+using mbd_host::Region;
+
+namespace {
+
+constexpr int64_t kMaxStride = (int64_t)1 << 24;
+
+struct Shape {
+  int64_t batch, tokens, heads, dk, dv, rows;
+  int g_bytes;
+};
+
+// Where a call's scratch lies, in bytes; see scan_plan.
+struct ScanPlan {
+  int nseg, L;
+  int32_t dkp, dvp;
+  int64_t heads;            // sequences x heads
+  size_t slots, slots2, sums, sums2, ends, qdq, bytes;
+};
+
+int64_t up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
+// Waves of a workgroup: two for at most 64 columns, else four.
+int waves_of(int64_t width) { return width <= 64 ? 2 : 4; }
+int out_cols(int64_t dv) {   // output columns per workgroup: even shares of at most 128
+  const int64_t nblk = (dv + 127) / 128, slabs = (dv + 31) / 32;
+  return (int)(32 * ((slabs + nblk - 1) / nblk));
+}
+
+// Sequences are cut into segments that run side by side when the heads alone
+// leave the GPU's 256 CUs (two workgroups each) idle.
+ScanPlan scan_plan(const gla_scan_t* p, bool backward) {
+  ScanPlan s = {};
+  s.dkp = (int32_t)up(p->dk, 32);
+  s.dvp = (int32_t)up(p->dv, 32);
+  s.heads = p->batch * p->heads;
+  const int64_t blocks = backward ? (p->dk + 127) / 128 : (p->dv + out_cols(p->dv) - 1) / out_cols(p->dv);
+  const int64_t units = s.heads * blocks;
+  constexpr int64_t kUnits = 512, kMinTokens = 128;
+  int64_t nseg = units > 0 ? (kUnits + units - 1) / units : 1;
+  nseg = std::min(nseg, p->tokens / kMinTokens);
+  nseg = std::max(nseg, (int64_t)1);
+  const int64_t L = std::max(up((p->tokens + nseg - 1) / nseg, mbd::kScanC), (int64_t)mbd::kScanC);
+  s.L = (int)L;
+  s.nseg = (int)std::max((p->tokens + L - 1) / L, (int64_t)1);
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    const size_t r = at;
+    at += (bytes + 255) / 256 * 256;
+    return r;
+  };
+  const size_t states = (size_t)s.heads * s.nseg * s.dkp * s.dvp * 4, chans = (size_t)s.heads * s.nseg * s.dkp * 4;
+  if (s.nseg > 1) {
+    s.slots = take(states);
+    s.sums = take(chans);
+    if (backward) {
+      s.slots2 = take(states);
+      s.sums2 = take(chans);
+    }
+  }
+  if (backward) {
+    s.ends = take(chans);
+    s.qdq = take((size_t)(p->offsets ? p->rows : p->batch * p->tokens) * p->heads * s.dkp * 4);
+  }
+  s.bytes = at;
+  return s;
+}
+
+Region region(const gla_scan_t* p, const void* x, const gla_stride_t& s, int64_t d, int64_t bytes) {
+  const int64_t b = p->offsets ? 1 : p->batch, t = p->offsets ? p->rows : p->tokens;
+  return Region{(uintptr_t)x, bytes, {b, t, p->heads}, {s.batch, s.token, s.head}, d};
+}
+
+bool strides_fit(const gla_scan_t* p, const gla_stride_t& s, int64_t d) {
+  const int64_t t = p->offsets ? p->rows : p->tokens;
+  if (s.head < 0 || s.head > ((int64_t)1 << 40)) return false;
+  if (!p->offsets && (s.batch < 0 || s.batch > ((int64_t)1 << 40))) return false;
+  return t <= 1 ? (s.token >= 0 && s.token <= kMaxStride) : (s.token >= d && s.token <= kMaxStride);
+}
+
+// Sizes and scalars; *idle: nothing to do.
+gemv_status_t check_sizes(const gla_scan_t* p, bool backward, bool* idle) {
+  *idle = false;
+  if (!p) return GEMV_ERR_INVALID_ARG;
+  if (p->dtype != GEMV_F16 && p->dtype != GEMV_BF16) return GEMV_ERR_UNSUPPORTED_DTYPE;
+  if (p->gate_f32 != 0 && p->gate_f32 != 1) return GEMV_ERR_UNSUPPORTED_DTYPE;
+  if (p->batch < 0 || p->tokens < 0 || p->heads < 0 || p->dk < 0 || p->dv < 0) return GEMV_ERR_INVALID_ARG;
+  if (p->offsets && p->rows < 0) return GEMV_ERR_INVALID_ARG;
+  if (p->batch == 0 || p->heads == 0 || p->dk == 0 || p->dv == 0) {
+    *idle = true;
+    return GEMV_OK;
+  }
+  const int64_t lim = (int64_t)1 << 30;
+  if (p->dk > 256 || p->dv > (backward ? 256 : 65536) || p->tokens > lim || (p->offsets && p->rows > lim) ||
+      p->batch > ((int64_t)1 << 20) || p->heads > ((int64_t)1 << 20) ||
+      p->batch * p->heads > ((int64_t)1 << 20))
+    return GEMV_ERR_TOO_LARGE;
+  if (!p->offsets && p->batch * p->tokens > ((int64_t)1 << 34)) return GEMV_ERR_TOO_LARGE;
+  if (p->offsets && ((uintptr_t)p->offsets & 3u)) return GEMV_ERR_MISALIGNED;
+  return GEMV_OK;
+}
+
+gemv_status_t check_inputs(const gla_scan_t* p, const void* q, const void* k, const void* v, const void* gk,
+                           const void* o) {
+  const int64_t rows = p->offsets ? p->rows : p->tokens;
+  if (rows > 0 && p->tokens > 0 && (!q || !k || !v || !gk || !o)) return GEMV_ERR_INVALID_ARG;
+  if (!strides_fit(p, p->q, p->dk) || !strides_fit(p, p->k, p->dk) || !strides_fit(p, p->v, p->dv) ||
+      !strides_fit(p, p->gk, p->dk) || !strides_fit(p, p->o, p->dv))
+    return GEMV_ERR_INVALID_ARG;
+  if (((uintptr_t)q | (uintptr_t)k | (uintptr_t)v | (uintptr_t)o) & 1u) return GEMV_ERR_MISALIGNED;
+  if ((uintptr_t)gk & (p->gate_f32 ? 3u : 1u)) return GEMV_ERR_MISALIGNED;
+  return GEMV_OK;
+}
+
+gemv_status_t check_scratch(const ScanPlan& s, const void* workspace, size_t bytes) {
+  if (s.bytes == 0) return GEMV_OK;
+  if (!workspace || bytes < s.bytes) return GEMV_ERR_INVALID_ARG;
+  if ((uintptr_t)workspace & 15u) return GEMV_ERR_MISALIGNED;
+  return GEMV_OK;
+}
+
+// Outputs against each other and against the inputs.
+bool clash(const Region* out, int no, const Region* in, int ni) {
+  for (int i = 0; i < no; ++i) {
+    if (out[i].empty()) continue;
+    if (!mbd_host::distinct(out[i])) return true;
+    for (int j = i + 1; j < no; ++j)
+      if (mbd_host::share(out[i], out[j])) return true;
+    for (int j = 0; j < ni; ++j)
+      if (mbd_host::share(out[i], in[j])) return true;
+  }
+  return false;
+}
+
+gemv_status_t check_forward(const gla_scan_t* p, const void* q, const void* k, const void* v, const void* gk,
+                            const float* S0, const float* ST, const void* o, const void* workspace,
+                            size_t workspace_bytes, bool* idle) {
+  gemv_status_t st = check_sizes(p, false, idle);
+  if (st != GEMV_OK || *idle) return st;
+  st = check_inputs(p, q, k, v, gk, o);
+  if (st != GEMV_OK) return st;
+  if (((uintptr_t)S0 | (uintptr_t)ST) & 3u) return GEMV_ERR_MISALIGNED;
+  const ScanPlan s = scan_plan(p, false);
+  st = check_scratch(s, workspace, workspace_bytes);
+  if (st != GEMV_OK) return st;
+  const int64_t state = s.heads * p->dk * p->dv, gb = p->gate_f32 ? 4 : 2;
+  const Region in[] = {region(p, q, p->q, p->dk, 2), region(p, k, p->k, p->dk, 2), region(p, v, p->v, p->dv, 2),
+                       region(p, gk, p->gk, p->dk, gb),
+                       mbd_host::dense_region(p->offsets, p->batch + 1, 4),
+                       mbd_host::dense_region(S0 == ST ? nullptr : S0, state, 4)};
+  const Region out[] = {region(p, o, p->o, p->dv, 2), mbd_host::dense_region(ST, state, 4),
+                        mbd_host::dense_region(s.bytes ? workspace : nullptr, (int64_t)s.bytes, 1)};
+  if (clash(out, 3, in, 6)) return GEMV_ERR_ALIASING;
+  return GEMV_OK;
+}
+
+gemv_status_t check_backward(const gla_scan_t* p, const gla_scan_grad_t* gr, const void* q, const void* k,
+                             const void* v, const void* gk, const float* S0, const void* dout, const float* dST,
+                             const void* dq, const void* dk, const void* dv, const void* dgk, const float* dS0,
+                             const void* workspace, size_t workspace_bytes, bool* idle) {
+  gemv_status_t st = check_sizes(p, true, idle);
+  if (st != GEMV_OK || *idle) return st;
+  if (!gr) return GEMV_ERR_INVALID_ARG;
+  st = check_inputs(p, q, k, v, gk, dout);
+  if (st != GEMV_OK) return st;
+  const int64_t rows = p->offsets ? p->rows : p->tokens;
+  if (rows > 0 && p->tokens > 0 && (!dq || !dk || !dv || !dgk)) return GEMV_ERR_INVALID_ARG;
+  if (!strides_fit(p, gr->dq, p->dk) || !strides_fit(p, gr->dk, p->dk) || !strides_fit(p, gr->dv, p->dv) ||
+      !strides_fit(p, gr->dgk, p->dk))
+    return GEMV_ERR_INVALID_ARG;
+  if (((uintptr_t)dq | (uintptr_t)dk | (uintptr_t)dv) & 1u) return GEMV_ERR_MISALIGNED;
+  if (((uintptr_t)dgk & (p->gate_f32 ? 3u : 1u)) || (((uintptr_t)S0 | (uintptr_t)dST | (uintptr_t)dS0) & 3u))
+    return GEMV_ERR_MISALIGNED;
+  const ScanPlan s = scan_plan(p, true);
+  st = check_scratch(s, workspace, workspace_bytes);
+  if (st != GEMV_OK) return st;
+  const int64_t state = s.heads * p->dk * p->dv, gb = p->gate_f32 ? 4 : 2;
+  const Region in[] = {region(p, q, p->q, p->dk, 2),     region(p, k, p->k, p->dk, 2),
+                       region(p, v, p->v, p->dv, 2),     region(p, gk, p->gk, p->dk, gb),
+                       region(p, dout, p->o, p->dv, 2),  mbd_host::dense_region(p->offsets, p->batch + 1, 4),
+                       mbd_host::dense_region(S0, state, 4), mbd_host::dense_region(dST, state, 4)};
+  const Region out[] = {region(p, dq, gr->dq, p->dk, 2),   region(p, dk, gr->dk, p->dk, 2),
+                        region(p, dv, gr->dv, p->dv, 2),   region(p, dgk, gr->dgk, p->dk, gb),
+                        mbd_host::dense_region(dS0, state, 4),
+                        mbd_host::dense_region(s.bytes ? workspace : nullptr, (int64_t)s.bytes, 1)};
+  if (clash(out, 6, in, 8)) return GEMV_ERR_ALIASING;
+  return GEMV_OK;
+}
+
+// ---- launches ------------------------------------------------------------------
+
+using mbd::ScanFn;
+using mbd::kScanGrad;
+using mbd::kScanOut;
+using mbd::kScanState;
+const size_t kOutLds[3] = {mbd::scan_out_lds<2>(), mbd::scan_out_lds<4>(), mbd::scan_out_lds<8>()};
+const size_t kGradLds[3] = {mbd::scan_grad_lds<2>(), mbd::scan_grad_lds<4>(), mbd::scan_grad_lds<8>()};
+
+// 64, 128 or 256 channels, by index.
+int tier(int64_t d) { return d <= 64 ? 0 : d <= 128 ? 1 : 2; }
+
+mbd::ScanTensor tensor(const gla_scan_t* p, const void* x, const gla_stride_t& s, int64_t d) {
+  mbd::ScanTensor t;
+  t.p = x;
+  t.sb = p->offsets ? 0 : s.batch;
+  t.sh = s.head;
+  t.st = (int32_t)s.token;
+  // 4-byte accesses: even channels, strides and a 4-byte aligned start
+  t.vec = d % 2 == 0 && (s.batch % 2 == 0 || p->offsets || p->batch == 1) && (s.head % 2 == 0 || p->heads == 1) &&
+          s.token % 2 == 0 && ((uintptr_t)x & 3u) == 0;
+  return t;
+}
+
+mbd::ScanArgs common(const gla_scan_t* p, const ScanPlan& s) {
+  mbd::ScanArgs a = {};
+  a.offsets = p->offsets;
+  a.total = p->rows;
+  a.t = p->tokens;
+  a.H = (int32_t)p->heads;
+  a.dk = (int32_t)p->dk;
+  a.dv = (int32_t)p->dv;
+  a.dkp = s.dkp;
+  a.dvp = s.dvp;
+  a.nseg = s.nseg;
+  a.L = s.L;
+  a.g32 = a.go32 = p->gate_f32;
+  return a;
+}
+
+hipError_t launch(ScanFn fn, int64_t grid, int waves, size_t lds, const mbd::ScanArgs& a, hipStream_t stream) {
+  void* args[] = {(void*)&a};
+  return hipLaunchKernel((const void*)fn, dim3((unsigned)grid), dim3((unsigned)waves * 64u), args, lds, stream);
+}
+
+hipError_t launch_join(const gla_scan_t* p, const ScanPlan& s, float* slots, const float* sums, const float* S0,
+                       int rev, hipStream_t stream) {
+  mbd::JoinArgs j = {slots, sums, S0, p->offsets, p->rows, p->tokens, (int32_t)p->heads, (int32_t)p->dk,
+                     (int32_t)p->dv, s.dkp, s.dvp, s.nseg, s.L, rev};
+  void* args[] = {(void*)&j};
+  const int64_t nx = ((int64_t)s.dkp * (s.dvp / 4) + 255) / 256;
+  return hipLaunchKernel((const void*)&mbd::scan_join_kernel, dim3((unsigned)(nx * s.heads)), dim3(256), args, 0,
+                         stream);
+}
+
+// A grid's work-items along x (a 32-bit field of the dispatch) are kept at most 2^31.
+bool grid_fits(int64_t grid, int threads) { return grid <= ((int64_t)1 << 31) / threads; }
+
+gemv_status_t on_device(gemv_handle_t h, const char* what) {
+  int dev = -1;
+  if (hipGetDevice(&dev) != hipSuccess) return report(h, GEMV_ERR_HIP, "hipGetDevice");
+  if (dev != h->device) return report(h, GEMV_ERR_WRONG_DEVICE, what);
+  return GEMV_OK;
+}
+
+}  // namespace
+
+bool mbd_host::scan_set_attributes() {
+  for (int d = 0; d < 2; ++d)
+    for (int r = 0; r < 2; ++r)
+      for (int t = 0; t < 3; ++t)
+        for (int w = 0; w < 2; ++w) {
+          const struct { ScanFn fn; size_t lds; } set[3] = {
+              {kScanOut[d][r][t][w], kOutLds[t]}, {kScanGrad[d][r][t][w], kGradLds[t]}, {kScanState[d][r][t][w], kGradLds[t]}};
+          for (const auto& x : set)
+            if (hipFuncSetAttribute((const void*)x.fn, hipFuncAttributeMaxDynamicSharedMemorySize, (int)x.lds) !=
+                hipSuccess)
+              return false;
+        }
+  return true;
+}
+
+extern "C" size_t gla_scan_workspace_bytes(const gla_scan_t* p, int32_t backward) {
+  bool idle = false;
+  if (check_sizes(p, backward != 0, &idle) != GEMV_OK || idle) return 0;
+  return scan_plan(p, backward != 0).bytes;
+}
+
+extern "C" gemv_status_t gla_scan_check_args(const gla_scan_t* p, const void* q, const void* k, const void* v,
+                                             const void* gk, const float* S0, const float* ST, const void* o,
+                                             const void* workspace, size_t workspace_bytes) {
+  bool idle;
+  return check_forward(p, q, k, v, gk, S0, ST, o, workspace, workspace_bytes, &idle);
+}
+
+extern "C" gemv_status_t gla_scan_grad_check_args(const gla_scan_t* p, const gla_scan_grad_t* grad, const void* q,
+                                                  const void* k, const void* v, const void* gk, const float* S0,
+                                                  const void* dout, const float* dST, const void* dq,
+                                                  const void* dk, const void* dv, const void* dgk,
+                                                  const float* dS0, const void* workspace,
+                                                  size_t workspace_bytes) {
+  bool idle;
+  return check_backward(p, grad, q, k, v, gk, S0, dout, dST, dq, dk, dv, dgk, dS0, workspace, workspace_bytes, &idle);
+}
+
+extern "C" gemv_status_t gla_scan_forward(gemv_handle_t h, const gla_scan_t* p, const void* q, const void* k,
+                                          const void* v, const void* gk, const float* S0, float* ST, void* o,
+                                          void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  if (!h || h->magic != kMagic) return report(nullptr, GEMV_ERR_NULL_HANDLE, "gla_scan_forward");
+  bool idle = false;
+  gemv_status_t st = check_forward(p, q, k, v, gk, S0, ST, o, workspace, workspace_bytes, &idle);
+  if (st != GEMV_OK) return report(h, st, "gla_scan_forward arguments");
+  if (idle || (p->tokens == 0 && !ST)) return GEMV_OK;
+  if ((st = on_device(h, "gla_scan_forward")) != GEMV_OK) return st;
+  const ScanPlan s = scan_plan(p, false);
+  const int64_t bh = s.heads;
+  mbd::ScanArgs a = common(p, s);
+  a.K = tensor(p, k, p->k, p->dk);
+  a.V = tensor(p, v, p->v, p->dv);
+  a.G = tensor(p, gk, p->gk, p->dk);
+  a.X = tensor(p, q, p->q, p->dk);
+  a.O = tensor(p, o, p->o, p->dv);
+  a.kscale = 1.0f;
+  a.oscale = p->scale;
+  a.S0 = S0;
+  a.ST = ST;
+  a.cols = out_cols(p->dv);
+  a.nblk = (int32_t)((p->dv + a.cols - 1) / a.cols);
+  const int64_t grid = bh * s.nseg * a.nblk;
+  if (!grid_fits(grid, 256)) return report(h, GEMV_ERR_TOO_LARGE, "gla_scan_forward grid");
+  hipError_t e = hipSuccess;
+  if (s.nseg > 1) {
+    char* w = (char*)workspace;
+    a.slots = (float*)(w + s.slots);
+    a.sums = (float*)(w + s.sums);
+    // a segment's own state: columns in blocks of at most 256, channels in blocks of a workgroup's
+    mbd::ScanArgs b = a;
+    const int kw = waves_of(p->dk);
+    b.nblk = (int32_t)((p->dk + 32 * kw - 1) / (32 * kw));
+    for (int64_t c0 = 0; c0 < p->dv && e == hipSuccess; c0 += 256) {
+      const int64_t c = std::min(p->dv - c0, (int64_t)256);
+      b.V.p = (const char*)a.V.p + c0 * 2;
+      b.dv = (int32_t)c;
+      b.ecol = (int32_t)c0;
+      e = launch(kScanState[p->dtype][0][tier(c)][kw == 4], bh * s.nseg * b.nblk, kw, kGradLds[tier(c)], b, stream);
+    }
+    if (e == hipSuccess) e = launch_join(p, s, a.slots, a.sums, S0, 0, stream);
+  }
+  const int ow = waves_of(a.cols);
+  if (e == hipSuccess) e = launch(kScanOut[p->dtype][0][tier(p->dk)][ow == 4], grid, ow, kOutLds[tier(p->dk)], a, stream);
+  return e == hipSuccess ? GEMV_OK : report(h, GEMV_ERR_HIP, hipGetErrorString(e));
+}
+
+extern "C" gemv_status_t gla_scan_backward(gemv_handle_t h, const gla_scan_t* p, const gla_scan_grad_t* grad,
+                                           const void* q, const void* k, const void* v, const void* gk,
+                                           const float* S0, const void* dout, const float* dST, void* dq, void* dk,
+                                           void* dv, void* dgk, float* dS0, void* workspace, size_t workspace_bytes,
+                                           hipStream_t stream) {
+  if (!h || h->magic != kMagic) return report(nullptr, GEMV_ERR_NULL_HANDLE, "gla_scan_backward");
+  bool idle = false;
+  gemv_status_t st = check_backward(p, grad, q, k, v, gk, S0, dout, dST, dq, dk, dv, dgk, dS0, workspace,
+                                    workspace_bytes, &idle);
+  if (st != GEMV_OK) return report(h, st, "gla_scan_backward arguments");
+  if (idle || (p->tokens == 0 && !dS0)) return GEMV_OK;
+  if ((st = on_device(h, "gla_scan_backward")) != GEMV_OK) return st;
+  const ScanPlan s = scan_plan(p, true);
+  char* w = (char*)workspace;
+  const mbd::ScanTensor tq = tensor(p, q, p->q, p->dk), tk = tensor(p, k, p->k, p->dk),
+                        tv = tensor(p, v, p->v, p->dv), tg = tensor(p, gk, p->gk, p->dk),
+                        tdo = tensor(p, dout, p->o, p->dv);
+  const int kw = waves_of(p->dk), cols = out_cols(p->dv), ow = waves_of(cols);
+  const int kt = tier(p->dk), vt = tier(p->dv), dt = p->dtype;
+  mbd::ScanArgs f = common(p, s), r = common(p, s);
+  f.G = r.G = tg;
+  f.nblk = r.nblk = (int32_t)((p->dk + 32 * kw - 1) / (32 * kw));
+  f.ends = r.ends = (float*)(w + s.ends);
+  f.qdq = r.qdq = (float*)(w + s.qdq);
+  f.K = tk;   // dq_i = scale S do_i
+  f.V = tv;
+  f.W = tdo;
+  f.X = tq;
+  f.O = tensor(p, dq, grad->dq, p->dk);
+  f.kscale = 1.0f;
+  f.oscale = p->scale;
+  f.S0 = S0;
+  f.dST = dST;
+  r.K = tq;   // dk_j = D v_j, with the scale in D
+  r.V = tdo;
+  r.W = tv;
+  r.X = tk;
+  r.O = tensor(p, dk, grad->dk, p->dk);
+  r.DG = tensor(p, dgk, grad->dgk, p->dk);
+  r.kscale = p->scale;
+  r.oscale = 1.0f;
+  r.S0 = dST;
+  r.ST = dS0;
+  mbd::ScanArgs o = r;   // dv_j = k_j^T D
+  o.X = tk;
+  o.O = tensor(p, dv, grad->dv, p->dv);
+  o.ST = nullptr;
+  o.cols = cols;
+  o.nblk = (int32_t)((p->dv + cols - 1) / cols);
+  const int64_t gk_grid = s.heads * s.nseg * f.nblk, gv_grid = s.heads * s.nseg * o.nblk;
+  if (!grid_fits(gk_grid, 256) || !grid_fits(gv_grid, 256))
+    return report(h, GEMV_ERR_TOO_LARGE, "gla_scan_backward grid");
+  hipError_t e = hipSuccess;
+  if (s.nseg > 1) {
+    f.slots = (float*)(w + s.slots);
+    f.sums = (float*)(w + s.sums);
+    r.slots = o.slots = (float*)(w + s.slots2);
+    r.sums = o.sums = (float*)(w + s.sums2);
+    f.others = r.slots;
+    e = launch(kScanState[dt][0][vt][kw == 4], gk_grid, kw, kGradLds[vt], f, stream);
+    if (e == hipSuccess) e = launch(kScanState[dt][1][vt][kw == 4], gk_grid, kw, kGradLds[vt], r, stream);
+    if (e == hipSuccess) e = launch_join(p, s, f.slots, f.sums, S0, 0, stream);
+    if (e == hipSuccess) e = launch_join(p, s, r.slots, r.sums, dST, 1, stream);
+  }
+  if (e == hipSuccess) e = launch(kScanGrad[dt][0][vt][kw == 4], gk_grid, kw, kGradLds[vt], f, stream);
+  if (e == hipSuccess) e = launch(kScanGrad[dt][1][vt][kw == 4], gk_grid, kw, kGradLds[vt], r, stream);
+  if (e == hipSuccess) e = launch(kScanOut[dt][1][kt][ow == 4], gv_grid, ow, kOutLds[kt], o, stream);
+  return e == hipSuccess ? GEMV_OK : report(h, GEMV_ERR_HIP, hipGetErrorString(e));
+}

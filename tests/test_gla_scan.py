@@ -1,0 +1,135 @@
+"""GPU: GLA over whole sequences (include/gla_scan.h), forward and backward,
+against the float64 recurrence of tests/scan_ref.py, whose bounds are derived
+there; 16-bit results add their one rounding, eps / 2 of the result (and half
+the smallest subnormal)."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import memory_bound_dense_amd as mbd
+import scan_ref
+from scan_ref import U
+
+pytestmark = pytest.mark.gpu
+BF, HF, F32 = torch.bfloat16, torch.float16, torch.float32
+
+
+@pytest.fixture(scope="module")
+def scan():
+    assert torch.cuda.is_available(), "GPU tests need a GPU"
+    g = mbd.Gemv()
+    yield mbd.GlaScan(g)
+    g.close()
+
+
+def inputs(b, t, h, dk, dv, dt, gt, gate=1.0, seed=0, state=True):
+    gen = torch.Generator().manual_seed(seed + 1000 * t + dk)
+    rnd = lambda *s: torch.randn(*s, generator=gen)
+    x = dict(q=rnd(b, t, h, dk).to(dt), k=(rnd(b, t, h, dk) / math.sqrt(dk)).to(dt),
+             v=rnd(b, t, h, dv).to(dt),
+             g=(torch.nn.functional.logsigmoid(rnd(b, t, h, dk)) / gate).to(gt),
+             do=rnd(b, t, h, dv).to(dt))
+    x["S0"] = rnd(b, h, dk, dv) if state else None
+    x["dST"] = rnd(b, h, dk, dv) if state else None
+    x["scale"] = 1.0 / math.sqrt(dk)
+    return x
+
+
+def f64(t):
+    return None if t is None else t.double().numpy()
+
+
+def cuda(x):
+    return {n: t.cuda() if torch.is_tensor(t) else t for n, t in x.items()}
+
+
+def step(dt):
+    """(relative, absolute) half step of a 16-bit type."""
+    f = torch.finfo(dt)
+    return (0.0, 0.0) if dt == F32 else (f.eps / 2, f.smallest_normal * f.eps / 2)
+
+
+def close(name, got, want, bound, dt):
+    got = got.double().cpu().numpy()
+    rel, tiny = step(dt)
+    bad = ~np.isfinite(got) | (np.abs(got - want) > bound + rel * (np.abs(want) + bound) + tiny)
+    assert not bad.any(), "%s: %d of %d off, worst %.3g of the bound, first %s" % (
+        name, bad.sum(), bad.size,
+        np.nanmax(np.abs(got - want) / (bound + rel * np.abs(want) + tiny + 1e-300)), np.argwhere(bad)[0])
+
+
+def fwd(scan, x, offsets=None, longest=None):
+    d = cuda(x)
+    nseq = x["q"].shape[0] if offsets is None else len(offsets) - 1
+    h, dk, dv = x["q"].shape[2], x["q"].shape[3], x["v"].shape[3]
+    o = torch.full_like(d["v"], float("nan"))
+    ST = torch.full((nseq, h, dk, dv), float("nan"), device="cuda")
+    off = None if offsets is None else torch.tensor(offsets, dtype=torch.int32, device="cuda")
+    scan.forward(d["q"], d["k"], d["v"], d["g"], o, x["scale"], S0=d["S0"], ST=ST, offsets=off,
+                 longest=longest)
+    torch.cuda.synchronize()
+    return o, ST
+
+
+def bwd(scan, x, offsets=None, longest=None):
+    d = cuda(x)
+    nan = lambda t: torch.full_like(t, float("nan"))
+    r = dict(dq=nan(d["q"]), dk=nan(d["k"]), dv=nan(d["v"]), dg=nan(d["g"]))
+    nseq = x["q"].shape[0] if offsets is None else len(offsets) - 1
+    h, dk, dv = x["q"].shape[2], x["q"].shape[3], x["v"].shape[3]
+    r["dS0"] = torch.full((nseq, h, dk, dv), float("nan"), device="cuda")
+    off = None if offsets is None else torch.tensor(offsets, dtype=torch.int32, device="cuda")
+    scan.backward(d["q"], d["k"], d["v"], d["g"], d["do"], r["dq"], r["dk"], r["dv"], r["dg"],
+                  x["scale"], S0=d["S0"], dST=d["dST"], dS0=r["dS0"], offsets=off, longest=longest)
+    torch.cuda.synchronize()
+    return r
+
+
+def check_fwd(x, o, ST, seq, rows, out=0):
+    """Sequence `seq` (state index `out`) at rows `rows` of batch entry 0 or seq."""
+    a = [f64(x[n][seq, rows]) for n in ("q", "k", "v", "g")]
+    S0 = None if x["S0"] is None else f64(x["S0"][out])
+    wo, wS, ao, aS = scan_ref.forward(*a, x["scale"], S0)
+    t = a[0].shape[0]
+    close("o", o[seq, rows], wo, scan_ref.rel16(t, a[3]) * ao, o.dtype)
+    close("ST", ST[out], wS, scan_ref.rel32(t, a[3]) * aS, F32)
+
+
+def check_bwd(x, r, seq, rows, out=0):
+    a = [f64(x[n][seq, rows]) for n in ("q", "k", "v", "g", "do")]
+    S0, dST = (None if x[n] is None else f64(x[n][out]) for n in ("S0", "dST"))
+    want, ab = scan_ref.backward(*a, x["scale"], S0, dST)
+    t, g = a[0].shape[0], a[3]
+    for n in ("dq", "dk", "dv"):
+        close(n, r[n][seq, rows], want[n], scan_ref.rel16(t, g) * ab[n], x["q"].dtype)
+    # q dq - k dk with both in three terms: the bound of a float32 result on each term
+    close("dg", r["dg"][seq, rows], want["dg"], 2 * scan_ref.rel32(t, g) * ab["dg_run"], x["g"].dtype)
+    close("dS0", r["dS0"][out], want["dS0"], scan_ref.rel32(t, g) * ab["dS0"], F32)
+
+
+SHAPES = [  # b, t, h, dk, dv
+    (1, 1, 1, 1, 1), (2, 1, 3, 128, 128), (1, 31, 2, 64, 64), (1, 32, 2, 32, 48), (2, 33, 1, 100, 36),
+    (1, 65, 2, 128, 128), (1, 129, 3, 17, 33), (1, 200, 1, 256, 256), (1, 300, 2, 128, 200),
+    (2, 290, 1, 160, 96), (1, 700, 1, 64, 128)]
+TYPES = [(BF, BF), (HF, HF), (BF, F32), (HF, F32)]
+TIDS = ["bf16", "f16", "bf16_g32", "f16_g32"]
+
+
+@pytest.mark.parametrize("b,t,h,dk,dv", SHAPES)
+@pytest.mark.parametrize("dt,gt", TYPES, ids=TIDS)
+def test_forward(scan, b, t, h, dk, dv, dt, gt):
+    x = inputs(b, t, h, dk, dv, dt, gt, gate=1.0 if t % 2 else 16.0, state=t != 65)
+    o, ST = fwd(scan, x)
+    for s in range(b):
+        check_fwd(x, o, ST, s, slice(None), s)
+
+
+@pytest.mark.parametrize("b,t,h,dk,dv", SHAPES)
+@pytest.mark.parametrize("dt,gt", TYPES, ids=TIDS)
+def test_backward(scan, b, t, h, dk, dv, dt, gt):
+    x = inputs(b, t, h, dk, dv, dt, gt, gate=1.0 if t % 2 else 16.0, state=t != 65)
+    r = bwd(scan, x)
+    for s in range(b):
+        check_bwd(x, r, s, slice(None), s)
