@@ -1,4 +1,5 @@
-"""ctypes binding of the operators around the GEMV: include/gla_scan.h.
+"""ctypes binding of the operators around the GEMV: include/gla_scan.h,
+include/gemm.h, include/rmsnorm.h.
 
 Argument marshalling only, as in ``_lib``: the C functions keep their names
 and return the C status codes (pointers are addresses as ints or None); the
@@ -17,9 +18,13 @@ from . import _lib
 from ._lib import (GEMV_ERR_INVALID_ARG, GEMV_ERR_UNSUPPORTED_DTYPE, GEMV_ERR_WRONG_DEVICE, GEMV_OK,
                    Gemv, GemvError, _check_devices, _dtype_code)
 
-# every symbol include/gla_scan.h declares
+# every symbol these headers declare
 OPERATOR_EXPORTS = ("gla_scan_workspace_bytes", "gla_scan_forward", "gla_scan_backward",
-                    "gla_scan_check_args", "gla_scan_grad_check_args")
+                    "gla_scan_check_args", "gla_scan_grad_check_args", "gemm_workspace_bytes",
+                    "gemm_run", "gemm_check_args", "rmsnorm_run", "rmsnorm_check_args")
+
+GEMM_F16, GEMM_BF16, GEMM_E4M3 = 0, 1, 2
+GEMM_ACTS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
 
 _vp, _i32, _i64, _st = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_int
 _sz, _f32 = ctypes.c_size_t, ctypes.c_float
@@ -41,6 +46,17 @@ class gla_scan_grad_t(ctypes.Structure):
                 ("dgk", gla_stride_t)]
 
 
+class gemm_t(ctypes.Structure):
+    _fields_ = [("m", _i64), ("n", _i64), ("k", _i64), ("lda", _i64), ("ldb", _i64), ("ldc", _i64),
+                ("ldr", _i64), ("in_type", _i32), ("dtype", _st), ("act", _i32), ("alpha", _f32),
+                ("scale_a", _vp), ("scale_b", _vp), ("bias", _vp), ("residual", _vp)]
+
+
+class rmsnorm_t(ctypes.Structure):
+    _fields_ = [("m", _i64), ("n", _i64), ("ldx", _i64), ("ldres", _i64), ("ldsum", _i64),
+                ("ldy", _i64), ("dtype", _st), ("out_e4m3", _i32), ("eps", _f32)]
+
+
 _ready = None
 
 
@@ -56,9 +72,16 @@ def load():
         lib.gla_scan_check_args.argtypes = [scan] + [_vp] * 7 + [_vp, _sz]
         lib.gla_scan_backward.argtypes = [_vp, scan, grad] + [_vp] * 12 + [_vp, _sz, _vp]
         lib.gla_scan_grad_check_args.argtypes = [scan, grad] + [_vp] * 12 + [_vp, _sz]
-        for name in ("gla_scan_forward", "gla_scan_check_args", "gla_scan_backward",
-                     "gla_scan_grad_check_args"):
-            getattr(lib, name).restype = _st
+        gemm, norm = ctypes.POINTER(gemm_t), ctypes.POINTER(rmsnorm_t)
+        lib.gemm_workspace_bytes.argtypes = [gemm]
+        lib.gemm_workspace_bytes.restype = _sz
+        lib.gemm_run.argtypes = [_vp, gemm, _vp, _vp, _vp, _vp, _sz, _vp]
+        lib.gemm_check_args.argtypes = [gemm, _vp, _vp, _vp, _vp, _sz]
+        lib.rmsnorm_run.argtypes = [_vp, norm] + [_vp] * 7
+        lib.rmsnorm_check_args.argtypes = [norm] + [_vp] * 6
+        for name in OPERATOR_EXPORTS:
+            if not name.endswith("_bytes"):
+                getattr(lib, name).restype = _st
         _ready = lib
     return _ready
 
@@ -90,6 +113,26 @@ def gla_scan_grad_check_args(p, grad, q, k, v, gk, S0, dout, dST, dq, dk, dv, dg
     return load().gla_scan_grad_check_args(ctypes.byref(p), ctypes.byref(grad), q, k, v, gk, S0,
                                            dout, dST, dq, dk, dv, dgk, dS0, workspace,
                                            workspace_bytes)
+
+
+def gemm_workspace_bytes(p):
+    return load().gemm_workspace_bytes(ctypes.byref(p))
+
+
+def gemm_run(h, p, A, B, C, workspace=None, workspace_bytes=0, stream=None):
+    return load().gemm_run(h, ctypes.byref(p), A, B, C, workspace, workspace_bytes, stream)
+
+
+def gemm_check_args(p, A, B, C, workspace=None, workspace_bytes=0):
+    return load().gemm_check_args(ctypes.byref(p), A, B, C, workspace, workspace_bytes)
+
+
+def rmsnorm_run(h, p, x, residual, w, sum_out, y, scales, stream=None):
+    return load().rmsnorm_run(h, ctypes.byref(p), x, residual, w, sum_out, y, scales, stream)
+
+
+def rmsnorm_check_args(p, x, residual, w, sum_out, y, scales):
+    return load().rmsnorm_check_args(ctypes.byref(p), x, residual, w, sum_out, y, scales)
 
 
 # ---- torch tensors -------------------------------------------------------------
@@ -223,3 +266,88 @@ class GlaScan:
         if s != GEMV_OK:
             raise GemvError(s, "gla_scan_backward")
         return dq, dk, dv, dgk
+
+
+def _rows(name, t, m, n, dtypes):
+    """Leading dimension of an (m, n) tensor with dense rows."""
+    if t.dim() != 2 or tuple(t.shape) != (m, n) or (n > 1 and t.stride(1) != 1):
+        raise _bad("%s %s, strides %s: want dense rows (%d, %d)" % (name, tuple(t.shape), t.stride(), m, n))
+    if t.dtype not in dtypes:
+        raise GemvError(GEMV_ERR_UNSUPPORTED_DTYPE, "%s is %s" % (name, t.dtype))
+    return t.stride(0) if m > 1 else max(t.stride(0), n)
+
+
+def _vector(name, t, n, dtype):
+    if t is not None and (t.dim() != 1 or t.shape[0] != n or not t.is_contiguous()):
+        raise _bad("%s must be a dense (%d,) tensor" % (name, n))
+    if t is not None and t.dtype != dtype:
+        raise GemvError(GEMV_ERR_UNSUPPORTED_DTYPE, "%s is %s" % (name, t.dtype))
+    return _ptr(t)
+
+
+class Gemm:
+    """C = act(alpha * scale_a[:, None] * scale_b * (A @ B.T) + bias) + residual
+    (include/gemm.h), through a Gemv handle.  A: (m, k) tokens, B: (n, k)
+    weights, both float16, bfloat16 or float8_e4m3fn; C, residual (m, n) and
+    bias (n,) of A's dtype (either 16-bit dtype with float8_e4m3fn); scales
+    float32.  residual may be C."""
+
+    def __init__(self, gemv=None):
+        self.g = gemv if gemv is not None else Gemv()
+
+    def __call__(self, A, B, C, bias=None, residual=None, act="none", alpha=1.0, scale_a=None,
+                 scale_b=None, workspace=None, stream=None):
+        import torch
+        if A.dim() != 2 or B.dim() != 2:
+            raise _bad("A and B must be 2-D")
+        if act not in GEMM_ACTS:
+            raise _bad("act %r: one of %s" % (act, ", ".join(GEMM_ACTS)))
+        (m, k), n = A.shape, B.shape[0]
+        e4m3 = A.dtype == torch.float8_e4m3fn
+        lda, ldb = _rows("A", A, m, k, (A.dtype,)), _rows("B", B, n, k, (A.dtype,))
+        ldc = _rows("C", C, m, n, (torch.float16, torch.bfloat16) if e4m3 else (A.dtype,))
+        p = gemm_t(m, n, k, lda, ldb, ldc, 0, GEMM_E4M3 if e4m3 else _dtype_code(A), _dtype_code(C),
+                   GEMM_ACTS[act], float(alpha), _vector("scale_a", scale_a, m, torch.float32),
+                   _vector("scale_b", scale_b, n, torch.float32), _vector("bias", bias, n, C.dtype))
+        if residual is not None:
+            p.ldr, p.residual = _rows("residual", residual, m, n, (C.dtype,)), residual.data_ptr()
+        _check_devices((B, C, bias, residual, scale_a, scale_b), A.device)
+        _on_current(A.device)
+        w, wp, wn = _scratch(workspace, gemm_workspace_bytes(p), A.device, stream)
+        s = gemm_run(self.g.h, p, A.data_ptr(), B.data_ptr(), C.data_ptr(), wp, wn,
+                     _stream_of(A.device, stream))
+        if s != GEMV_OK:
+            raise GemvError(s, "gemm_run")
+        return C
+
+
+class RmsNorm:
+    """Root-mean-square norm over rows (include/rmsnorm.h), through a Gemv
+    handle: s = x + residual (stored in sum_out if given), y = s *
+    rsqrt(mean(s^2) + eps) * w.  y of x's dtype, or float8_e4m3fn with float32
+    ``scales`` (m,)."""
+
+    def __init__(self, gemv=None):
+        self.g = gemv if gemv is not None else Gemv()
+
+    def __call__(self, x, w, y, eps=1e-6, residual=None, sum_out=None, scales=None, stream=None):
+        import torch
+        if x.dim() != 2:
+            raise _bad("x must be 2-D")
+        m, n = x.shape
+        e4m3 = y.dtype == torch.float8_e4m3fn
+        p = rmsnorm_t(m, n, _rows("x", x, m, n, (x.dtype,)), 0, 0,
+                      _rows("y", y, m, n, (x.dtype, torch.float8_e4m3fn)), _dtype_code(x), int(e4m3),
+                      float(eps))
+        if residual is not None:
+            p.ldres = _rows("residual", residual, m, n, (x.dtype,))
+        if sum_out is not None:
+            p.ldsum = _rows("sum_out", sum_out, m, n, (x.dtype,))
+        wp, sp = _vector("w", w, n, x.dtype), _vector("scales", scales, m, torch.float32)
+        _check_devices((w, y, residual, sum_out, scales), x.device)
+        _on_current(x.device)
+        s = rmsnorm_run(self.g.h, p, x.data_ptr(), _ptr(residual), wp, _ptr(sum_out), y.data_ptr(),
+                        sp, _stream_of(x.device, stream))
+        if s != GEMV_OK:
+            raise GemvError(s, "rmsnorm_run")
+        return y

@@ -17,11 +17,12 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libgemv.so")
 SOURCES = [os.path.join(CSRC, f) for f in ("gemv.hip", "gla.hip", "gla_scan.hip", "gla_scan_out.hip",
-                                             "gla_scan_grad.hip", "gla_scan_state.hip")]
+                                             "gla_scan_grad.hip", "gla_scan_state.hip", "gemm.hip",
+                                             "rmsnorm.hip")]
 DEPS = SOURCES + [os.path.join(CSRC, f) for f in ("gemv_kernel.h", "gemv_shift.h", "gemv_staged.h", "gla_kernel.h",
-                                                     "gla_scan_kernel.h", "gla_scan_table.h", "handle.h",
+                                                     "gla_scan_kernel.h", "gla_scan_table.h", "gemm_kernel.h", "handle.h",
                                                      "operand.h")] + \
-    [os.path.join(INCLUDE, f) for f in ("gemv.h", "gla_decode.h", "gla_scan.h")]
+    [os.path.join(INCLUDE, f) for f in ("gemv.h", "gla_decode.h", "gla_scan.h", "gemm.h", "rmsnorm.h")]
 # measurement aid: a plain streaming read (the practical HBM read ceiling)
 PROBE_LIB = os.path.join(PKG, "libmbd_probe.so")
 PROBE_SOURCES = [os.path.join(CSRC, "stream_probe.hip")]

@@ -1,0 +1,191 @@
+// libgemv.so, continued: the dense product of many rows with its epilogue
+// (include/gemm.h) over the kernels of gemm_kernel.h.
+#include "gemm.h"
+
+#include "gemm_kernel.h"
+#include "handle.h"
+#include "operand.h"
+
+using mbd_host::kMagic;
+using mbd_host::Region;
+
+namespace {
+
+int64_t in_bytes(int32_t type) { return type == GEMM_E4M3 ? 1 : 2; }
+int64_t up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
+
+using GemmFn = void (*)(const mbd::GemmArgs);
+
+// Tiles: rows of B x tokens.
+struct Tile {
+  int bn, bm, threads;
+  size_t lds;
+  GemmFn fn[3];
+};
+#define TILE(BN, BM, WN, WM)                                                                      \
+  {BN, BM, WN * WM * 64, mbd::gemm_tile_lds<BN, BM>(),                                            \
+   {&mbd::gemm_tile_kernel<0, BN, BM, WN, WM>, &mbd::gemm_tile_kernel<1, BN, BM, WN, WM>,         \
+    &mbd::gemm_tile_kernel<2, BN, BM, WN, WM>}}
+const Tile kTiles[] = {TILE(256, 256, 2, 4), TILE(128, 256, 2, 2), TILE(128, 128, 2, 2), TILE(64, 128, 2, 2),
+                       TILE(64, 64, 2, 2)};
+constexpr int kNumTiles = sizeof(kTiles) / sizeof(kTiles[0]);
+
+constexpr int kSkinnyWaves = 8;
+#define SKINNY(MT, U) \
+  {&mbd::gemm_skinny_kernel<0, MT, 8, U>, &mbd::gemm_skinny_kernel<1, MT, 8, U>, &mbd::gemm_skinny_kernel<2, MT, 8, U>}
+const GemmFn kSkinny[2][3] = {SKINNY(1, 4), SKINNY(2, 2)};
+
+struct GemmPlan {
+  int tile;          // -1: skinny
+  int mt;            // skinny: token tiles
+  int64_t tiles_m, tiles_n, nsplit, npad;
+  size_t bytes;
+};
+
+GemmPlan gemm_plan(const gemm_t* p) {
+  GemmPlan g = {};
+  const int64_t slabs = (p->k * in_bytes(p->in_type) + 127) / 128;
+  g.nsplit = 1;
+  if (p->m <= 32) {
+    g.tile = -1;
+    g.mt = p->m <= 16 ? 1 : 2;
+    g.tiles_m = 1;
+    g.tiles_n = (p->n + 15) / 16;
+    const int64_t want = (256 + g.tiles_n - 1) / g.tiles_n;
+    g.nsplit = std::max(std::min(want, slabs / (kSkinnyWaves * 2)), (int64_t)1);
+  } else {
+    // the largest tile that still gives every CU one
+    g.tile = kNumTiles - 1;
+    for (int t = 0; t < kNumTiles; ++t) {
+      const int64_t c = ((p->m + kTiles[t].bm - 1) / kTiles[t].bm) * ((p->n + kTiles[t].bn - 1) / kTiles[t].bn);
+      if (c >= 256) {
+        g.tile = t;
+        break;
+      }
+    }
+    g.tiles_m = (p->m + kTiles[g.tile].bm - 1) / kTiles[g.tile].bm;
+    g.tiles_n = (p->n + kTiles[g.tile].bn - 1) / kTiles[g.tile].bn;
+    const int64_t want = 256 / (g.tiles_m * g.tiles_n);
+    g.nsplit = std::max(std::min(want, slabs / 8), (int64_t)1);
+  }
+  g.npad = up(p->n, 4);
+  if (g.tile < 0) g.npad = up(p->n, 16);
+  if (g.nsplit > 1) g.bytes = (size_t)g.nsplit * p->m * g.npad * 4;
+  return g;
+}
+
+Region matrix(const void* x, int64_t rows, int64_t cols, int64_t ld, int64_t bytes) {
+  return Region{(uintptr_t)x, bytes, {rows, 1, 1}, {ld, 0, 0}, cols};
+}
+
+gemv_status_t check(const gemm_t* p, const void* A, const void* B, const void* C, const void* workspace,
+                    size_t workspace_bytes, bool sizes_only) {
+  if (!p) return GEMV_ERR_INVALID_ARG;
+  if (p->in_type < GEMM_F16 || p->in_type > GEMM_E4M3) return GEMV_ERR_UNSUPPORTED_DTYPE;
+  if (p->dtype != GEMV_F16 && p->dtype != GEMV_BF16) return GEMV_ERR_UNSUPPORTED_DTYPE;
+  if (p->in_type != GEMM_E4M3 && p->in_type != (int32_t)p->dtype) return GEMV_ERR_UNSUPPORTED_DTYPE;
+  if (p->act < GEMM_ACT_NONE || p->act > GEMM_ACT_SILU) return GEMV_ERR_INVALID_ARG;
+  if (p->m < 0 || p->n < 0 || p->k < 0) return GEMV_ERR_INVALID_ARG;
+  if (p->m == 0 || p->n == 0) return GEMV_OK;
+  const int64_t e = in_bytes(p->in_type), lim = (int64_t)1 << 30;
+  if (p->m > lim || p->n > lim || p->k > lim) return GEMV_ERR_TOO_LARGE;
+  if (p->lda < p->k || p->ldb < p->k || p->ldc < p->n || (p->residual && p->ldr < p->n)) return GEMV_ERR_INVALID_ARG;
+  if (p->lda > ((int64_t)1 << 23) / e || p->ldb > ((int64_t)1 << 23) / e || p->ldc > lim ||
+      (p->residual && p->ldr > lim))
+    return GEMV_ERR_TOO_LARGE;
+  if (sizes_only) return GEMV_OK;
+  if (!C || (p->k > 0 && (!A || !B))) return GEMV_ERR_INVALID_ARG;
+  uintptr_t two = (uintptr_t)C | (uintptr_t)p->bias | (uintptr_t)p->residual;
+  if (e == 2 && p->k > 0) two |= (uintptr_t)A | (uintptr_t)B;
+  if ((two & 1u) || (((uintptr_t)p->scale_a | (uintptr_t)p->scale_b) & 3u)) return GEMV_ERR_MISALIGNED;
+  const GemmPlan g = gemm_plan(p);
+  if (g.bytes) {
+    if (!workspace || workspace_bytes < g.bytes) return GEMV_ERR_INVALID_ARG;
+    if ((uintptr_t)workspace & 15u) return GEMV_ERR_MISALIGNED;
+  }
+  const bool in_place = p->residual == C && p->ldr == p->ldc;
+  const Region in[] = {matrix(p->k > 0 ? A : nullptr, p->m, p->k, p->lda, e),
+                       matrix(p->k > 0 ? B : nullptr, p->n, p->k, p->ldb, e),
+                       mbd_host::dense_region(p->scale_a, p->m, 4), mbd_host::dense_region(p->scale_b, p->n, 4),
+                       mbd_host::dense_region(p->bias, p->n, 2),
+                       matrix(in_place ? nullptr : p->residual, p->m, p->n, p->ldr, 2)};
+  const Region out[] = {matrix(C, p->m, p->n, p->ldc, 2),
+                        mbd_host::dense_region(g.bytes ? workspace : nullptr, (int64_t)g.bytes, 1)};
+  for (const Region& o : out) {
+    for (const Region& i : in)
+      if (mbd_host::share(o, i)) return GEMV_ERR_ALIASING;
+  }
+  if (mbd_host::share(out[0], out[1])) return GEMV_ERR_ALIASING;
+  return GEMV_OK;
+}
+
+}  // namespace
+
+bool mbd_host::gemm_set_attributes() {
+  for (const Tile& t : kTiles)
+    for (GemmFn f : t.fn)
+      if (hipFuncSetAttribute((const void*)f, hipFuncAttributeMaxDynamicSharedMemorySize, (int)t.lds) != hipSuccess)
+        return false;
+  return true;
+}
+
+extern "C" size_t gemm_workspace_bytes(const gemm_t* p) {
+  if (check(p, nullptr, nullptr, nullptr, nullptr, 0, true) != GEMV_OK || p->m == 0 || p->n == 0) return 0;
+  return gemm_plan(p).bytes;
+}
+
+extern "C" gemv_status_t gemm_check_args(const gemm_t* p, const void* A, const void* B, const void* C,
+                                         const void* workspace, size_t workspace_bytes) {
+  return check(p, A, B, C, workspace, workspace_bytes, false);
+}
+
+extern "C" gemv_status_t gemm_run(gemv_handle_t h, const gemm_t* p, const void* A, const void* B, void* C,
+                                  void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  if (!h || h->magic != kMagic) return report(nullptr, GEMV_ERR_NULL_HANDLE, "gemm_run");
+  gemv_status_t st = check(p, A, B, C, workspace, workspace_bytes, false);
+  if (st != GEMV_OK) return report(h, st, "gemm_run arguments");
+  if (p->m == 0 || p->n == 0) return GEMV_OK;
+  int dev = -1;
+  if (hipGetDevice(&dev) != hipSuccess) return report(h, GEMV_ERR_HIP, "hipGetDevice");
+  if (dev != h->device) return report(h, GEMV_ERR_WRONG_DEVICE, "gemm_run");
+  const GemmPlan g = gemm_plan(p);
+  const int64_t e = in_bytes(p->in_type);
+  mbd::GemmArgs a = {};
+  a.A = (const uint8_t*)A;
+  a.B = (const uint8_t*)B;
+  a.C = (uint16_t*)C;
+  a.sa = p->scale_a;
+  a.sb = p->scale_b;
+  a.bias = (const uint16_t*)p->bias;
+  a.res = (const uint16_t*)p->residual;
+  a.part = (float*)workspace;
+  a.lda = p->lda * e;
+  a.ldb = p->ldb * e;
+  a.ldc = p->ldc;
+  a.ldr = p->residual ? p->ldr : 0;
+  a.m = (int32_t)p->m;
+  a.n = (int32_t)p->n;
+  a.kbytes = (int32_t)(p->k * e);
+  a.act = p->act;
+  a.out = p->dtype;
+  a.vec = p->ldc % 4 == 0 && ((uintptr_t)C & 7u) == 0 &&
+          (!p->residual || (p->ldr % 4 == 0 && ((uintptr_t)p->residual & 7u) == 0));
+  a.tiles_m = (int32_t)g.tiles_m;
+  a.tiles_n = (int32_t)g.tiles_n;
+  a.nsplit = (int32_t)g.nsplit;
+  a.npad = (int32_t)g.npad;
+  a.alpha = p->alpha;
+  const int64_t grid = g.tiles_m * g.tiles_n * g.nsplit;
+  const int threads = g.tile < 0 ? kSkinnyWaves * 64 : kTiles[g.tile].threads;
+  const int64_t jgrid = g.nsplit > 1 ? (p->m * (g.npad / 4) + 255) / 256 : 0;
+  // a grid's work-items along x (a 32-bit field of the dispatch) are kept at most 2^31
+  if (grid > ((int64_t)1 << 31) / threads || jgrid > ((int64_t)1 << 23))
+    return report(h, GEMV_ERR_TOO_LARGE, "gemm_run grid");
+  void* args[] = {(void*)&a};
+  const void* fn = (const void*)(g.tile < 0 ? kSkinny[g.mt - 1][p->in_type] : kTiles[g.tile].fn[p->in_type]);
+  hipError_t err = hipLaunchKernel(fn, dim3((unsigned)grid), dim3((unsigned)threads), args,
+                                   g.tile < 0 ? 0 : kTiles[g.tile].lds, stream);
+  if (err == hipSuccess && g.nsplit > 1)
+    err = hipLaunchKernel((const void*)&mbd::gemm_join_kernel, dim3((unsigned)jgrid), dim3(256), args, 0, stream);
+  return err == hipSuccess ? GEMV_OK : report(h, GEMV_ERR_HIP, hipGetErrorString(err));
+}

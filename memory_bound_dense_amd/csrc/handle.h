@@ -21,6 +21,7 @@ constexpr int kMaxVariants = 96;
 
 // Kernel attributes of the other operators on the current device, set by gemv_create.
 bool scan_set_attributes();
+bool gemm_set_attributes();
 
 }  // namespace mbd_host
 
