@@ -16,9 +16,10 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libgemv.so")
-SOURCES = [os.path.join(CSRC, f) for f in ("gemv.hip", "gla.hip", "gla_scan.hip", "gla_scan_out.hip",
-                                             "gla_scan_grad.hip", "gla_scan_state.hip", "gemm.hip",
-                                             "rmsnorm.hip")]
+SOURCES = [os.path.join(CSRC, f) for f in (
+    "gemv.hip", "gla_scan_out_f16.hip", "gla_scan_out_bf16.hip", "gla_scan_grad_f16.hip",
+    "gla_scan_grad_bf16.hip", "gla_scan_state_f16.hip", "gla_scan_state_bf16.hip", "gemm.hip", "gla.hip",
+    "gla_scan.hip", "rmsnorm.hip")]
 DEPS = SOURCES + [os.path.join(CSRC, f) for f in ("gemv_kernel.h", "gemv_shift.h", "gemv_staged.h", "gla_kernel.h",
                                                      "gla_scan_kernel.h", "gla_scan_table.h", "gemm_kernel.h", "handle.h",
                                                      "operand.h")] + \

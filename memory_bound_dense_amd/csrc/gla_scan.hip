@@ -246,9 +246,13 @@ gemv_status_t check_backward(const gla_scan_t* p, const gla_scan_grad_t* gr, con
 // ---- launches ------------------------------------------------------------------
 
 using mbd::ScanFn;
-using mbd::kScanGrad;
-using mbd::kScanOut;
-using mbd::kScanState;
+using mbd::ScanForms;
+const ScanForms* const kScanOut[2] = {&mbd::kScanOutF16, &mbd::kScanOutBf16};
+const ScanForms* const kScanGrad[2] = {&mbd::kScanGradF16, &mbd::kScanGradBf16};
+const ScanForms* const kScanState[2] = {&mbd::kScanStateF16, &mbd::kScanStateBf16};
+ScanFn scan_form(const ScanForms* const (&forms)[2], const gla_scan_t* p, int rev, int tier, bool four) {
+  return (*forms[p->dtype])[p->gate_f32][rev][tier][four];
+}
 const size_t kOutLds[3] = {mbd::scan_out_lds<2>(), mbd::scan_out_lds<4>(), mbd::scan_out_lds<8>()};
 const size_t kGradLds[3] = {mbd::scan_grad_lds<2>(), mbd::scan_grad_lds<4>(), mbd::scan_grad_lds<8>()};
 
@@ -279,7 +283,6 @@ mbd::ScanArgs common(const gla_scan_t* p, const ScanPlan& s) {
   a.dvp = s.dvp;
   a.nseg = s.nseg;
   a.L = s.L;
-  a.g32 = a.go32 = p->gate_f32;
   return a;
 }
 
@@ -311,17 +314,18 @@ gemv_status_t on_device(gemv_handle_t h, const char* what) {
 }  // namespace
 
 bool mbd_host::scan_set_attributes() {
-  for (int d = 0; d < 2; ++d)
-    for (int r = 0; r < 2; ++r)
-      for (int t = 0; t < 3; ++t)
-        for (int w = 0; w < 2; ++w) {
-          const struct { ScanFn fn; size_t lds; } set[3] = {
-              {kScanOut[d][r][t][w], kOutLds[t]}, {kScanGrad[d][r][t][w], kGradLds[t]}, {kScanState[d][r][t][w], kGradLds[t]}};
-          for (const auto& x : set)
-            if (hipFuncSetAttribute((const void*)x.fn, hipFuncAttributeMaxDynamicSharedMemorySize, (int)x.lds) !=
+  const auto set = [](const ScanForms* forms, const size_t (&lds)[3]) {
+    for (const auto& g : *forms)
+      for (const auto& r : g)
+        for (int t = 0; t < 3; ++t)
+          for (ScanFn fn : r[t])
+            if (hipFuncSetAttribute((const void*)fn, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds[t]) !=
                 hipSuccess)
               return false;
-        }
+    return true;
+  };
+  for (int d = 0; d < 2; ++d)
+    if (!set(kScanOut[d], kOutLds) || !set(kScanGrad[d], kGradLds) || !set(kScanState[d], kGradLds)) return false;
   return true;
 }
 
@@ -387,12 +391,12 @@ extern "C" gemv_status_t gla_scan_forward(gemv_handle_t h, const gla_scan_t* p, 
       b.V.p = (const char*)a.V.p + c0 * 2;
       b.dv = (int32_t)c;
       b.ecol = (int32_t)c0;
-      e = launch(kScanState[p->dtype][0][tier(c)][kw == 4], bh * s.nseg * b.nblk, kw, kGradLds[tier(c)], b, stream);
+      e = launch(scan_form(kScanState, p, 0, tier(c), kw == 4), bh * s.nseg * b.nblk, kw, kGradLds[tier(c)], b, stream);
     }
     if (e == hipSuccess) e = launch_join(p, s, a.slots, a.sums, S0, 0, stream);
   }
   const int ow = waves_of(a.cols);
-  if (e == hipSuccess) e = launch(kScanOut[p->dtype][0][tier(p->dk)][ow == 4], grid, ow, kOutLds[tier(p->dk)], a, stream);
+  if (e == hipSuccess) e = launch(scan_form(kScanOut, p, 0, tier(p->dk), ow == 4), grid, ow, kOutLds[tier(p->dk)], a, stream);
   return e == hipSuccess ? GEMV_OK : report(h, GEMV_ERR_HIP, hipGetErrorString(e));
 }
 
@@ -414,7 +418,7 @@ extern "C" gemv_status_t gla_scan_backward(gemv_handle_t h, const gla_scan_t* p,
                         tv = tensor(p, v, p->v, p->dv), tg = tensor(p, gk, p->gk, p->dk),
                         tdo = tensor(p, dout, p->o, p->dv);
   const int kw = waves_of(p->dk), cols = out_cols(p->dv), ow = waves_of(cols);
-  const int kt = tier(p->dk), vt = tier(p->dv), dt = p->dtype;
+  const int kt = tier(p->dk), vt = tier(p->dv);
   mbd::ScanArgs f = common(p, s), r = common(p, s);
   f.G = r.G = tg;
   f.nblk = r.nblk = (int32_t)((p->dk + 32 * kw - 1) / (32 * kw));
@@ -455,13 +459,13 @@ extern "C" gemv_status_t gla_scan_backward(gemv_handle_t h, const gla_scan_t* p,
     r.slots = o.slots = (float*)(w + s.slots2);
     r.sums = o.sums = (float*)(w + s.sums2);
     f.others = r.slots;
-    e = launch(kScanState[dt][0][vt][kw == 4], gk_grid, kw, kGradLds[vt], f, stream);
-    if (e == hipSuccess) e = launch(kScanState[dt][1][vt][kw == 4], gk_grid, kw, kGradLds[vt], r, stream);
+    e = launch(scan_form(kScanState, p, 0, vt, kw == 4), gk_grid, kw, kGradLds[vt], f, stream);
+    if (e == hipSuccess) e = launch(scan_form(kScanState, p, 1, vt, kw == 4), gk_grid, kw, kGradLds[vt], r, stream);
     if (e == hipSuccess) e = launch_join(p, s, f.slots, f.sums, S0, 0, stream);
     if (e == hipSuccess) e = launch_join(p, s, r.slots, r.sums, dST, 1, stream);
   }
-  if (e == hipSuccess) e = launch(kScanGrad[dt][0][vt][kw == 4], gk_grid, kw, kGradLds[vt], f, stream);
-  if (e == hipSuccess) e = launch(kScanGrad[dt][1][vt][kw == 4], gk_grid, kw, kGradLds[vt], r, stream);
-  if (e == hipSuccess) e = launch(kScanOut[dt][1][kt][ow == 4], gv_grid, ow, kOutLds[kt], o, stream);
+  if (e == hipSuccess) e = launch(scan_form(kScanGrad, p, 0, vt, kw == 4), gk_grid, kw, kGradLds[vt], f, stream);
+  if (e == hipSuccess) e = launch(scan_form(kScanGrad, p, 1, vt, kw == 4), gk_grid, kw, kGradLds[vt], r, stream);
+  if (e == hipSuccess) e = launch(scan_form(kScanOut, p, 1, kt, ow == 4), gv_grid, ow, kOutLds[kt], o, stream);
   return e == hipSuccess ? GEMV_OK : report(h, GEMV_ERR_HIP, hipGetErrorString(e));
 }

@@ -84,7 +84,7 @@ struct ScanArgs {
   float* ends;             // grad: rowsum(S D) at the end of each segment, [dkp]
   float* qdq;              // grad: q dq, (rows, H, dkp) float32
   int64_t t;               // tokens per sequence (the longest, if packed)
-  int32_t H, dk, dv, dkp, dvp, nseg, L, nblk, cols, g32, go32;
+  int32_t H, dk, dv, dkp, dvp, nseg, L, nblk, cols;
   int32_t ecol;            // state-only: first of the dv columns that V holds, in the slots
   float kscale, oscale;
 };
@@ -192,14 +192,19 @@ __device__ __forceinline__ f32x4 mfma_terms(const bf16x8 (&a)[NA], const bf16x8 
 // from the chunk's first token.  Offsets behind the chunk's last valid token
 // fall out of the descriptor's range: loads give 0, stores do nothing.
 struct Lane {
-  uint32_t off0, off1, step;   // bytes: channel 0, channel 1 (of the lane's lowest token), token stride
+  uint32_t off0, step;   // bytes: channel 0 of the lane's lowest token, token stride
+  bool lone;             // channel 1 is behind the last one
 };
+template <int BYTES>
+__device__ __forceinline__ uint32_t off1_of(const Lane& l) {
+  return l.lone ? kOffsetOutOfRange : l.off0 + BYTES;   // beyond the range where off0 is
+}
 template <bool REV>
 __device__ __forceinline__ Lane lane_of(const ScanTensor& x, int g, int c0, int width, int bytes) {
   const uint32_t row = (uint32_t)(REV ? 24 - 8 * g : 8 * g) * (uint32_t)x.st;
   Lane l;
   l.off0 = c0 < width ? (row + (uint32_t)c0) * bytes : kOffsetOutOfRange;
-  l.off1 = c0 + 1 < width ? (row + (uint32_t)c0 + 1u) * bytes : kOffsetOutOfRange;
+  l.lone = c0 + 1 == width;
   l.step = (uint32_t)x.st * bytes;
   return l;
 }
@@ -209,21 +214,29 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t chunk_rsrc(const ScanTensor& x
   const uint32_t len = n > 0 ? ((uint32_t)(n - 1) * (uint32_t)x.st + (uint32_t)width) * bytes : 0u;
   return make_rsrc(base + tok * (int64_t)x.st * bytes, len);
 }
+// The lane's offsets as the loop's own values: the 8 tokens' offsets are then
+// formed where they are used, not kept in 8 registers per tensor over the loop.
+__device__ __forceinline__ Lane fresh(Lane l) {
+  asm volatile("" : "+v"(l.off0));
+  return l;
+}
 // Token j (0..7) of the lane, in the order of the recurrence.
 template <bool REV>
 __device__ __forceinline__ uint32_t tok_off(const Lane& l, int j) {
   return (uint32_t)(REV ? 7 - j : j) * l.step;
 }
 template <bool REV>
-__device__ __forceinline__ void load16(__amdgpu_buffer_rsrc_t r, const Lane& l, int vec, uint32_t (&w)[8]) {
+__device__ __forceinline__ void load16(__amdgpu_buffer_rsrc_t r, const Lane& kept, int vec, uint32_t (&w)[8]) {
+  const Lane l = fresh(kept);
   if (vec) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) w[j] = __builtin_amdgcn_raw_buffer_load_b32(r, l.off0 + tok_off<REV>(l, j), 0, 0);
   } else {
+    const uint32_t off1 = off1_of<2>(l);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const uint32_t a = __builtin_amdgcn_raw_buffer_load_b16(r, l.off0 + tok_off<REV>(l, j), 0, 0);
-      const uint32_t b = __builtin_amdgcn_raw_buffer_load_b16(r, l.off1 + tok_off<REV>(l, j), 0, 0);
+      const uint32_t b = __builtin_amdgcn_raw_buffer_load_b16(r, off1 + tok_off<REV>(l, j), 0, 0);
       w[j] = (a & 0xffffu) | (b << 16);
     }
   }
@@ -234,25 +247,31 @@ __device__ __forceinline__ void store16(__amdgpu_buffer_rsrc_t r, const Lane& l,
     __builtin_amdgcn_raw_buffer_store_b32(w, r, l.off0 + tok_off<REV>(l, j), 0, 0);
   } else {
     __builtin_amdgcn_raw_buffer_store_b16((uint16_t)w, r, l.off0 + tok_off<REV>(l, j), 0, 0);
-    __builtin_amdgcn_raw_buffer_store_b16((uint16_t)(w >> 16), r, l.off1 + tok_off<REV>(l, j), 0, 0);
+    __builtin_amdgcn_raw_buffer_store_b16((uint16_t)(w >> 16), r, off1_of<2>(l) + tok_off<REV>(l, j), 0, 0);
   }
 }
 // The gates of the lane's two channels: raw words, 8 (16-bit) or 16 (float32).
-template <bool REV>
-__device__ __forceinline__ void load_gates(__amdgpu_buffer_rsrc_t r, const Lane& l, int vec, int g32,
-                                           uint32_t (&w)[16]) {
-  if (g32) {
+template <bool G32> constexpr int kGateWords = G32 ? 16 : 8;
+template <bool REV, bool G32>
+__device__ __forceinline__ void load_gates(__amdgpu_buffer_rsrc_t r, const Lane& kept, int vec,
+                                           uint32_t (&w)[kGateWords<G32>]) {
+  const Lane l = fresh(kept);
+  if constexpr (G32) {
+    const uint32_t off1 = off1_of<4>(l);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       w[2 * j] = __builtin_amdgcn_raw_buffer_load_b32(r, l.off0 + tok_off<REV>(l, j), 0, 0);
-      w[2 * j + 1] = __builtin_amdgcn_raw_buffer_load_b32(r, l.off1 + tok_off<REV>(l, j), 0, 0);
+      w[2 * j + 1] = __builtin_amdgcn_raw_buffer_load_b32(r, off1 + tok_off<REV>(l, j), 0, 0);
     }
   } else {
-    uint32_t p[8];
-    load16<REV>(r, l, vec, p);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) w[j] = p[j];
+    load16<REV>(r, l, vec, w);
   }
+}
+// Channel c of token j.
+template <int DT, bool G32>
+__device__ __forceinline__ float gate_value(const uint32_t (&w)[kGateWords<G32>], int c, int j) {
+  if constexpr (G32) return __builtin_bit_cast(float, w[2 * j + c]);
+  else return c ? pair_hi<DT>(w[j]) : pair_lo<DT>(w[j]);
 }
 
 // A chunk's gates for the lane's two channels and 8 tokens.
@@ -263,63 +282,66 @@ struct Gates {
   float sum[2];       // end
   bool hard;
 };
-template <int DT>
-__device__ __forceinline__ void gate_values(const uint32_t (&w)[16], int g32, float (&x)[2][8]) {
-  if (g32) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      x[0][j] = __builtin_bit_cast(float, w[2 * j]);
-      x[1][j] = __builtin_bit_cast(float, w[2 * j + 1]);
-    }
-  } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      x[0][j] = pair_lo<DT>(w[j]);
-      x[1][j] = pair_hi<DT>(w[j]);
-    }
-  }
+// Gates are summed as whole multiples of 2^-24 in units of log 2: exact sums,
+// each gate within 2^-25, and an exponential is a table-free 2^fraction scaled
+// by the whole part.  Summed in fp32, chunks of strong gates lose up to 2^-24
+// |G| (1e-6 at |G| = 20) in every decay.
+constexpr float kFix = 16777216.0f * 1.44269504f;
+constexpr int32_t kFixRange = (int32_t)(kRange * kFix);        // |G - r| (at most 88.7: 31 bits)
+constexpr int32_t kFixSum = 2100000000;                        // |G|: sums that reach it may have saturated
+__device__ __forceinline__ int32_t add_sat(int32_t a, int32_t b) { return __builtin_elementwise_add_sat(a, b); }
+__device__ __forceinline__ int32_t abs_of(int32_t x) { return max(x, -x); }
+// 2^(d / 2^24) and its reciprocal
+__device__ __forceinline__ void exp_pair(int32_t d, float& up, float& down) {
+  const int32_t whole = d >> 24;
+  const float p = __builtin_amdgcn_exp2f((float)(d & 0xffffff) * 5.9604644775390625e-8f);
+  up = __builtin_amdgcn_ldexpf(p, whole);
+  down = __builtin_amdgcn_ldexpf(__builtin_amdgcn_rcpf(p), -whole);
 }
-// e^x to fp32 rounding for |x| <= kRange: the product x log2(e) in two parts.
-__device__ __forceinline__ float exp_of(float x) {
-  const float y = x * 1.44269502f;
-  const float lo = __builtin_fmaf(x, 1.44269502f, -y) + x * 1.92596299e-8f;
-  const float p = __builtin_amdgcn_exp2f(y);
-  return __builtin_fmaf(p, lo * 0.693147182f, p);
+__device__ __forceinline__ float exp_fix(int32_t d) {
+  return __builtin_amdgcn_ldexpf(__builtin_amdgcn_exp2f((float)(d & 0xffffff) * 5.9604644775390625e-8f), d >> 24);
 }
-template <bool REV>
-__device__ __forceinline__ void make_gates(const float (&x)[2][8], int lane, Gates& q) {
+template <int DT, bool G32, bool REV, bool UP = true>
+__device__ __forceinline__ void make_gates(const uint32_t (&w)[kGateWords<G32>], int lane, Gates& q) {
   const int g = lane >> 4;
-  q.hard = false;
+  uint32_t wild = 0;
+  int32_t far = 0, sum = 0;
 #pragma unroll
   for (int c = 0; c < 2; ++c) {
-    float run = 0.0f, G[8];
+    int32_t run = 0, G[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
+      const float x = gate_value<DT, G32>(w, c, j);
+      wild = max(wild, __builtin_bit_cast(uint32_t, x) & 0x7fffffffu);
       if (REV) G[j] = run;
-      run += x[c][j];
+      run = add_sat(run, (int32_t)__builtin_rintf(x * kFix));   // the conversion saturates
       if (!REV) G[j] = run;
     }
-    float a = run;
-    const float u = __shfl_up(a, 16, 64);
-    if (g >= 1) a += u;
-    const float v = __shfl_up(a, 32, 64);
-    if (g >= 2) a += v;
-    const float before = __shfl_up(a, 16, 64);
-    const float mid = __shfl(a, 16 + (lane & 15), 64);
-    const float end = __shfl(a, 48 + (lane & 15), 64);
-    const float base = g >= 1 ? before : 0.0f;
+    int32_t a = run;
+    const int32_t u = __shfl_up(a, 16, 64);
+    if (g >= 1) a = add_sat(a, u);
+    const int32_t v = __shfl_up(a, 32, 64);
+    if (g >= 2) a = add_sat(a, v);
+    const int32_t before = __shfl_up(a, 16, 64);
+    const int32_t mid = __shfl(a, 16 + (lane & 15), 64);
+    const int32_t end = __shfl(a, 48 + (lane & 15), 64);
+    const int32_t base = g >= 1 ? before : 0;
+    sum = max(sum, max(abs_of(a), abs_of(end)));
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const float d = (base + G[j]) - mid;
-      q.hard |= !(__builtin_fabsf(d) <= kRange);
-      q.up[c][j] = exp_of(d);
-      q.down[c][j] = exp_of(-d);
+      const int32_t x = add_sat(base, G[j]);
+      const int32_t d = __builtin_elementwise_sub_sat(x, mid);
+      sum = max(sum, abs_of(x));
+      far = max(far, abs_of(d));
+      exp_pair(d, q.up[c][j], q.down[c][j]);
     }
-    q.hard |= !(mid <= kRange) || !(end - mid <= kRange);
-    q.a[c] = expf(mid);
-    q.b[c] = expf(end - mid);
-    q.sum[c] = end;
+    far = max(far, max(mid, __builtin_elementwise_sub_sat(end, mid)));
+    q.a[c] = exp_fix(mid);
+    q.b[c] = exp_fix(__builtin_elementwise_sub_sat(end, mid));
+    q.sum[c] = (float)end * (1.0f / kFix);
   }
+  // NaN and gates beyond 80 (their fixed-point form has saturated) in `wild`
+  q.hard = wild > 0x42a00000u || far > kFixRange || sum > kFixSum;
 }
 
 __device__ __forceinline__ uint32_t mag(float x) { return __builtin_bit_cast(uint32_t, x) & 0x7fffffffu; }
@@ -339,6 +361,12 @@ __device__ __forceinline__ void columns_of(const uint32_t (&w)[8], u32x4& c0, u3
   }
 }
 
+// xcd_unit for grids below 2^31.
+__device__ __forceinline__ uint32_t xcd_unit32(uint32_t b, uint32_t G) {
+  const uint32_t x = b % kXcds, q = G / kXcds, r = G % kXcds;
+  return x * q + min(x, r) + b / kXcds;
+}
+
 // The sequence, head, segment and block of a workgroup.  Workgroups that read
 // the same rows (a segment's blocks) are neighbours on one XCD.
 struct Place {
@@ -351,14 +379,14 @@ struct Place {
   bool last;          // the sequence's last segment
 };
 __device__ __forceinline__ bool place_of(const ScanArgs& a, Place& p) {
-  int64_t u = xcd_unit(blockIdx.x, gridDim.x);
-  p.blk = (int)(u % a.nblk);
-  u /= a.nblk;
+  uint32_t u = (uint32_t)xcd_unit32(blockIdx.x, gridDim.x);
+  p.blk = (int)(u % (uint32_t)a.nblk);
+  u /= (uint32_t)a.nblk;
   p.slot = u;
-  p.seg = (int)(u % a.nseg);
-  u /= a.nseg;
-  p.h = (int)(u % a.H);
-  p.seq = (int)(u / a.H);
+  p.seg = (int)(u % (uint32_t)a.nseg);
+  u /= (uint32_t)a.nseg;
+  p.h = (int)(u % (uint32_t)a.H);
+  p.seq = (int)(u / (uint32_t)a.H);
   p.row0 = 0;
   p.b = p.seq;
   p.len = a.t;
@@ -384,6 +412,63 @@ __device__ __forceinline__ int row_of(int m, int tile) { return 8 * (m >> 2) + 4
 constexpr int kPadRow = 8;              // 16-bit elements behind each row of a staged tile
 constexpr int kTokRow = kScanC + 8;     // tokens per row of a transposed tile, padded
 
+// The tokens [pos, pos + width) that a step takes: the whole chunk (32), or, where
+// the gates or values do not allow it, 8 (those of one lane group) or 1.
+struct Step {
+  int pos, width;
+};
+__device__ __forceinline__ bool takes(const Step& t, int g, int j) {
+  return (uint32_t)(8 * g + j - t.pos) < (uint32_t)t.width;
+}
+// What a step that was refused is tried with, and the step after `t`.
+__device__ __forceinline__ void smaller(Step& t) { t.width = t.width == 32 ? 8 : 1; }
+__device__ __forceinline__ void advance(Step& t) {
+  t.pos += t.width;
+  if ((t.pos & 7) == 0 && t.width == 1) t.width = 8;
+}
+// The words of the step's tokens; others read as 0.
+__device__ __forceinline__ void take(const Step& t, int g, const uint32_t (&from)[8], uint32_t (&to)[8]) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) to[j] = from[j];
+  if (t.width != 32) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (!takes(t, g, j)) to[j] = 0u;
+  }
+}
+// Gates of a step: of the chunk, of 8 tokens (the others' are 0), or of one
+// token, whose decay acts as a whole before it (forward) or after it (reversed)
+// and needs no pair of factors -- so it may be 0, infinite or NaN.
+template <int DT, bool G32, bool REV>
+__device__ __forceinline__ void step_gates(const Step& t, const uint32_t (&gw)[kGateWords<G32>], int lane, Gates& q) {
+  const int g = lane >> 4;
+  if (t.width == 1) {
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      float x = 0.0f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        q.up[c][j] = q.down[c][j] = 1.0f;
+        x = (t.pos & 7) == j ? gate_value<DT, G32>(gw, c, j) : x;
+      }
+      x = __shfl(x, 2 * (t.pos & ~7) + (lane & 15), 64);
+      q.sum[c] = x;
+      q.a[c] = REV ? 1.0f : expf(x);
+      q.b[c] = REV ? expf(x) : 1.0f;
+    }
+    q.hard = false;
+    return;
+  }
+  uint32_t w[kGateWords<G32>];
+#pragma unroll
+  for (int j = 0; j < kGateWords<G32>; ++j) w[j] = gw[j];
+  if (t.width == 8 && g != t.pos >> 3) {
+#pragma unroll
+    for (int j = 0; j < kGateWords<G32>; ++j) w[j] = 0u;
+  }
+  make_gates<DT, G32, REV>(w, lane, q);
+}
+
 // ---- out_i = X_i^T S ---------------------------------------------------------
 // A wave owns 32 columns of the state (64 VGPRs at DK 128) and of the output;
 // X e^{G-r} and K e^{r-G} are computed once per workgroup, 32 channels per
@@ -395,16 +480,17 @@ constexpr size_t scan_out_lds() {
          (size_t)2 * NS * 32 * 4 + 64;
 }
 
-template <int DT, int NS, int NW, bool REV>
-__global__ __launch_bounds__(NW * 64, 2) void scan_out_kernel(const ScanArgs a) {
+template <int DT, bool G32, int NS, int NW, bool REV>
+__global__ __launch_bounds__(NW * 64, NS > 4 ? 1 : 2) void scan_out_kernel(const ScanArgs a) {
   constexpr int DKP = NS * 32, RS = DKP + kPadRow;
+  constexpr int gb = G32 ? 4 : 2;
+  constexpr int SL = (NS + NW - 1) / NW;              // slabs of 32 channels a wave stages
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
   uint16_t* xs = (uint16_t*)smem;                     // X e^{G-r}: 2 terms of [32][RS]
   uint16_t* ks = xs + 2 * kScanC * RS;                // K e^{r-G}: 2 terms of [32][RS]
   uint16_t* kt = ks + 2 * kScanC * RS;                // the same, 3 terms of [DKP][kTokRow]
   float* dec = (float*)(kt + 3 * DKP * kTokRow);      // e^{r} [DKP], e^{end-r} [DKP]
   int* wild = (int*)(dec + 2 * DKP);                  // one flag per wave
-  float* seqx = (float*)smem;                         // token by token: X, K, e^g as [32][DKP] each
 
   Place p;
   if (!place_of(a, p)) return;
@@ -412,7 +498,6 @@ __global__ __launch_bounds__(NW * 64, 2) void scan_out_kernel(const ScanArgs a) 
   const int n = lane & 15, g = lane >> 4;
   const int col = p.blk * a.cols + wave * 32 + 2 * n;     // the lane's output columns col, col + 1
   const int vwidth = min(a.dv, (p.blk + 1) * a.cols);
-  const int gb = a.g32 ? 4 : 2;
 
   f32x4 S[NS][2][2];
   if (!a.slots) {
@@ -447,35 +532,52 @@ __global__ __launch_bounds__(NW * 64, 2) void scan_out_kernel(const ScanArgs a) 
   const char *kb = base_of(a.K, p, 2), *vb = base_of(a.V, p, 2), *xb = base_of(a.X, p, 2),
              *gbp = base_of(a.G, p, gb), *ob = base_of(a.O, p, 2);
   const Lane vl = lane_of<REV>(a.V, g, col, vwidth, 2), ol = lane_of<REV>(a.O, g, col, vwidth, 2);
-
+  Lane xl[SL], kl[SL], gl[SL];
+#pragma unroll
+  for (int i = 0; i < SL; ++i) {
+    const int d0 = 32 * (wave + i * NW) + 2 * n;     // beyond dk: nothing is loaded
+    xl[i] = lane_of<REV>(a.X, g, d0, a.dk, 2);
+    kl[i] = lane_of<REV>(a.K, g, d0, a.dk, 2);
+    gl[i] = lane_of<REV>(a.G, g, d0, a.dk, gb);
+  }
   const int nch = (int)((p.hi - p.lo + kScanC - 1) / kScanC);
-  for (int c = 0; c < nch; ++c) {
+  uint32_t vw[8], xw[SL][8], kw[SL][8], gw[SL][kGateWords<G32>];
+  auto fetch = [&](int c) {
+    const int64_t tok = p.lo + (int64_t)(REV ? nch - 1 - c : c) * kScanC;
+    const int nv = (int)min((int64_t)kScanC, p.hi - tok);
+    const auto gr = chunk_rsrc(a.G, gbp, tok, nv, a.dk, gb), kr = chunk_rsrc(a.K, kb, tok, nv, a.dk, 2),
+               xr = chunk_rsrc(a.X, xb, tok, nv, a.dk, 2);
+#pragma unroll
+    for (int i = 0; i < SL; ++i) {
+      load_gates<REV, G32>(gr, gl[i], a.G.vec, gw[i]);
+      load16<REV>(kr, kl[i], a.K.vec, kw[i]);
+      load16<REV>(xr, xl[i], a.X.vec, xw[i]);
+    }
+    load16<REV>(chunk_rsrc(a.V, vb, tok, nv, a.dv, 2), vl, a.V.vec, vw);
+  };
+  if (nch > 0) fetch(0);
+  Step st = {0, 32};
+  for (int c = 0; c < nch;) {
     const int64_t tok = p.lo + (int64_t)(REV ? nch - 1 - c : c) * kScanC;
     const int nv = (int)min((int64_t)kScanC, p.hi - tok);
     bool hard = false;
-    uint32_t vw[8];
-    load16<REV>(chunk_rsrc(a.V, vb, tok, nv, a.dv, 2), vl, a.V.vec, vw);
-    // the staged slabs of 32 channels
-    for (int s = wave; s < NS; s += NW) {
-      const int d0 = 32 * s + 2 * n;
-      uint32_t xw[8], kw[8], gw[16];
-      const Lane xl = lane_of<REV>(a.X, g, d0, a.dk, 2), kl = lane_of<REV>(a.K, g, d0, a.dk, 2),
-                 gl = lane_of<REV>(a.G, g, d0, a.dk, gb);
-      load_gates<REV>(chunk_rsrc(a.G, gbp, tok, nv, a.dk, gb), gl, a.G.vec, a.g32, gw);
-      load16<REV>(chunk_rsrc(a.K, kb, tok, nv, a.dk, 2), kl, a.K.vec, kw);
-      load16<REV>(chunk_rsrc(a.X, xb, tok, nv, a.dk, 2), xl, a.X.vec, xw);
-      float gv[2][8];
-      gate_values<DT>(gw, a.g32, gv);
+#pragma unroll
+    for (int i = 0; i < SL; ++i) {
+      const int s = wave + i * NW, d0 = 32 * s + 2 * n;
+      if (NS % NW != 0 && s >= NS) break;
       Gates q;
-      make_gates<REV>(gv, lane, q);
+      step_gates<DT, G32, REV>(st, gw[i], lane, q);
+      uint32_t xt[8], kv[8];
+      take(st, g, xw[i], xt);
+      take(st, g, kw[i], kv);
       float kf[2][8];
       uint32_t big = 0;
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const int row = 8 * g + j;
-        const float x0 = pair_lo<DT>(xw[j]) * q.up[0][j], x1 = pair_hi<DT>(xw[j]) * q.up[1][j];
-        kf[0][j] = pair_lo<DT>(kw[j]) * a.kscale * q.down[0][j];
-        kf[1][j] = pair_hi<DT>(kw[j]) * a.kscale * q.down[1][j];
+        const float x0 = pair_lo<DT>(xt[j]) * q.up[0][j], x1 = pair_hi<DT>(xt[j]) * q.up[1][j];
+        kf[0][j] = pair_lo<DT>(kv[j]) * a.kscale * q.down[0][j];
+        kf[1][j] = pair_hi<DT>(kv[j]) * a.kscale * q.down[1][j];
         big = max(max(big, max(mag(x0), mag(x1))), max(mag(kf[0][j]), mag(kf[1][j])));
         uint32_t t[2];
         split2<2>(x0, x1, t);
@@ -490,7 +592,7 @@ __global__ __launch_bounds__(NW * 64, 2) void scan_out_kernel(const ScanArgs a) 
         bf16x8 t[3];
         split8<3>(kf[nt], t);
 #pragma unroll
-        for (int i = 0; i < 3; ++i) *(bf16x8*)(kt + (i * DKP + d0 + nt) * kTokRow + 8 * g) = t[i];
+        for (int m = 0; m < 3; ++m) *(bf16x8*)(kt + (m * DKP + d0 + nt) * kTokRow + 8 * g) = t[m];
         if (g == 0) {
           dec[d0 + nt] = q.a[nt];
           dec[DKP + d0 + nt] = q.b[nt];
@@ -498,150 +600,99 @@ __global__ __launch_bounds__(NW * 64, 2) void scan_out_kernel(const ScanArgs a) 
       }
       hard |= q.hard || big > kBigBits;
     }
+    uint32_t vv[8];
+    take(st, g, vw, vv);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) hard |= pair_wild<DT>(vw[j]);
+    for (int j = 0; j < 8; ++j) hard |= pair_wild<DT>(vv[j]);
     const bool any = __ballot(hard) != 0;
     if (lane == 0) wild[wave] = any;
     __syncthreads();
     int all = 0;
 #pragma unroll
     for (int w = 0; w < NW; ++w) all |= wild[w];
+    if (st.width > 1 && __builtin_amdgcn_readfirstlane(all)) {
+      smaller(st);
+      __syncthreads();
+      continue;
+    }
 
+    u32x4 vc[2];
+    columns_of(vv, vc[0], vc[1]);
+    const Step now = st;
+    advance(st);
+    const int next = st.pos == kScanC ? c + 1 : c;
+    if (next != c) {
+      st = Step{0, 32};
+      if (next < nch) fetch(next);   // in flight during the products
+    }
     f32x4 o[2][2] = {};
-    if (!__builtin_amdgcn_readfirstlane(all)) {
-      f32x4 pt[2][2] = {};   // scores, transposed: rows j, columns i
+    f32x4 pt[2][2] = {};   // scores, transposed: rows j, columns i
 #pragma unroll
-      for (int s = 0; s < NS; ++s) {
-        bf16x8 kk[2][2], xx[2][2];
+    for (int s = 0; s < NS; ++s) {
+      bf16x8 kk[2][2], xx[2][2];
 #pragma unroll
-        for (int tl = 0; tl < 2; ++tl)
+      for (int tl = 0; tl < 2; ++tl)
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            kk[tl][i] = *(const bf16x8*)(ks + (i * kScanC + row_of(n, tl)) * RS + 32 * s + 8 * g);
-            xx[tl][i] = *(const bf16x8*)(xs + (i * kScanC + row_of(n, tl)) * RS + 32 * s + 8 * g);
-          }
-#pragma unroll
-        for (int jt = 0; jt < 2; ++jt)
-#pragma unroll
-          for (int it = 0; it < 2; ++it) pt[jt][it] = mfma_terms<2, 2>(kk[jt], xx[it], pt[jt][it]);
-        f32x4 d0 = *(const f32x4*)(dec + 32 * s + 8 * g), d1 = *(const f32x4*)(dec + 32 * s + 8 * g + 4);
-#pragma unroll
-        for (int nt = 0; nt < 2; ++nt) {
-          S[s][0][nt] *= d0;
-          S[s][1][nt] *= d1;
-          float x[8];
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            x[r] = S[s][0][nt][r];
-            x[4 + r] = S[s][1][nt][r];
-          }
-          bf16x8 st[2];
-          split8<2>(x, st);
-#pragma unroll
-          for (int it = 0; it < 2; ++it) o[it][nt] = mfma_terms<2, 2>(xx[it], st, o[it][nt]);
+        for (int i = 0; i < 2; ++i) {
+          kk[tl][i] = *(const bf16x8*)(ks + (i * kScanC + row_of(n, tl)) * RS + 32 * s + 8 * g);
+          xx[tl][i] = *(const bf16x8*)(xs + (i * kScanC + row_of(n, tl)) * RS + 32 * s + 8 * g);
         }
-      }
-      u32x4 vc[2];
-      columns_of(vw, vc[0], vc[1]);
-      bf16x8 vt[2][kTerms<DT>];
-      exact_terms<DT>(vc[0], vt[0]);
-      exact_terms<DT>(vc[1], vt[1]);
 #pragma unroll
-      for (int it = 0; it < 2; ++it) {
+      for (int jt = 0; jt < 2; ++jt)
+#pragma unroll
+        for (int it = 0; it < 2; ++it) pt[jt][it] = mfma_terms<2, 2>(kk[jt], xx[it], pt[jt][it]);
+      f32x4 d0 = *(const f32x4*)(dec + 32 * s + 8 * g), d1 = *(const f32x4*)(dec + 32 * s + 8 * g + 4);
+#pragma unroll
+      for (int nt = 0; nt < 2; ++nt) {
+        S[s][0][nt] *= d0;
+        S[s][1][nt] *= d1;
         float x[8];
 #pragma unroll
-        for (int jt = 0; jt < 2; ++jt)
-#pragma unroll
-          for (int r = 0; r < 4; ++r) x[4 * jt + r] = 8 * g + 4 * jt + r <= row_of(n, it) ? pt[jt][it][r] : 0.0f;
-        bf16x8 ps[2];
-        split8<2>(x, ps);
-#pragma unroll
-        for (int nt = 0; nt < 2; ++nt) o[it][nt] = mfma_terms(ps, vt[nt], o[it][nt]);
-      }
-#pragma unroll
-      for (int s = 0; s < NS; ++s)
-#pragma unroll
-        for (int tl = 0; tl < 2; ++tl) {
-          bf16x8 kk[3];
-#pragma unroll
-          for (int i = 0; i < 3; ++i)
-            kk[i] = *(const bf16x8*)(kt + (i * DKP + 32 * s + row_of(n, tl)) * kTokRow + 8 * g);
-          const f32x4 d = *(const f32x4*)(dec + DKP + 32 * s + 8 * g + 4 * tl);
-#pragma unroll
-          for (int nt = 0; nt < 2; ++nt) S[s][tl][nt] = mfma_terms(kk, vt[nt], S[s][tl][nt]) * d;
+        for (int r = 0; r < 4; ++r) {
+          x[r] = S[s][0][nt][r];
+          x[4 + r] = S[s][1][nt][r];
         }
-    } else {
-      // the recurrence itself: X, K and e^g of the chunk in fp32 through LDS
-      __syncthreads();
-      for (int s = wave; s < NS; s += NW) {
-        const int d0 = 32 * s + 2 * n;
-        uint32_t xw[8], kw[8], gw[16];
-        const Lane xl = lane_of<REV>(a.X, g, d0, a.dk, 2), kl = lane_of<REV>(a.K, g, d0, a.dk, 2),
-                   gl = lane_of<REV>(a.G, g, d0, a.dk, gb);
-        load_gates<REV>(chunk_rsrc(a.G, gbp, tok, nv, a.dk, gb), gl, a.G.vec, a.g32, gw);
-        load16<REV>(chunk_rsrc(a.K, kb, tok, nv, a.dk, 2), kl, a.K.vec, kw);
-        load16<REV>(chunk_rsrc(a.X, xb, tok, nv, a.dk, 2), xl, a.X.vec, xw);
-        float gv[2][8];
-        gate_values<DT>(gw, a.g32, gv);
+        bf16x8 sx[2];
+        split8<2>(x, sx);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          float* to = seqx + (8 * g + j) * DKP + d0;
-          *(f32x2*)to = f32x2{pair_lo<DT>(xw[j]), pair_hi<DT>(xw[j])};
-          *(f32x2*)(to + kScanC * DKP) = f32x2{pair_lo<DT>(kw[j]) * a.kscale, pair_hi<DT>(kw[j]) * a.kscale};
-          *(f32x2*)(to + 2 * kScanC * DKP) = f32x2{expf(gv[0][j]), expf(gv[1][j])};
-        }
-      }
-      __syncthreads();
-      for (int tg = 0; tg < 4; ++tg) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float* from = seqx + (8 * tg + j) * DKP;
-          const uint32_t w = __shfl(vw[j], 16 * tg + n, 64);
-          const float v0 = pair_lo<DT>(w), v1 = pair_hi<DT>(w);
-          // a token behind the end changes nothing (its gate and k are 0)
-          float s0 = 0.0f, s1 = 0.0f;
-#pragma unroll
-          for (int s = 0; s < NS; ++s)
-#pragma unroll
-            for (int tl = 0; tl < 2; ++tl) {
-              const int d = 32 * s + 8 * g + 4 * tl;
-              const f32x4 x = *(const f32x4*)(from + d), k = *(const f32x4*)(from + kScanC * DKP + d),
-                          e = *(const f32x4*)(from + 2 * kScanC * DKP + d);
-#pragma unroll
-              for (int r = 0; r < 4; ++r) {
-                float y0 = S[s][tl][0][r], y1 = S[s][tl][1][r];
-                if (!REV) {
-                  y0 *= e[r];
-                  y1 *= e[r];
-                }
-                y0 = __builtin_fmaf(k[r], v0, y0);
-                y1 = __builtin_fmaf(k[r], v1, y1);
-                s0 = __builtin_fmaf(x[r], y0, s0);
-                s1 = __builtin_fmaf(x[r], y1, s1);
-                if (REV) {
-                  y0 *= e[r];
-                  y1 *= e[r];
-                }
-                S[s][tl][0][r] = y0;
-                S[s][tl][1][r] = y1;
-              }
-            }
-          s0 += __shfl_xor(s0, 16, 64);
-          s1 += __shfl_xor(s1, 16, 64);
-          s0 += __shfl_xor(s0, 32, 64);
-          s1 += __shfl_xor(s1, 32, 64);
-          if (g == tg) {
-            o[j >> 2][0][j & 3] = s0;
-            o[j >> 2][1][j & 3] = s1;
-          }
-        }
+        for (int it = 0; it < 2; ++it) o[it][nt] = mfma_terms<2, 2>(xx[it], sx, o[it][nt]);
       }
     }
+    bf16x8 vt[2][kTerms<DT>];
+    exact_terms<DT>(vc[0], vt[0]);
+    exact_terms<DT>(vc[1], vt[1]);
+#pragma unroll
+    for (int it = 0; it < 2; ++it) {
+      float x[8];
+#pragma unroll
+      for (int jt = 0; jt < 2; ++jt)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) x[4 * jt + r] = 8 * g + 4 * jt + r <= row_of(n, it) ? pt[jt][it][r] : 0.0f;
+      bf16x8 ps[2];
+      split8<2>(x, ps);
+#pragma unroll
+      for (int nt = 0; nt < 2; ++nt) o[it][nt] = mfma_terms(ps, vt[nt], o[it][nt]);
+    }
+#pragma unroll
+    for (int s = 0; s < NS; ++s)
+#pragma unroll
+      for (int tl = 0; tl < 2; ++tl) {
+        bf16x8 kk[3];
+#pragma unroll
+        for (int i = 0; i < 3; ++i)
+          kk[i] = *(const bf16x8*)(kt + (i * DKP + 32 * s + row_of(n, tl)) * kTokRow + 8 * g);
+        const f32x4 d = *(const f32x4*)(dec + DKP + 32 * s + 8 * g + 4 * tl);
+#pragma unroll
+        for (int nt = 0; nt < 2; ++nt) S[s][tl][nt] = mfma_terms(kk, vt[nt], S[s][tl][nt]) * d;
+      }
     const __amdgpu_buffer_rsrc_t orsrc = chunk_rsrc(a.O, ob, tok, nv, a.dv, 2);
+    const Lane ot = fresh(ol);
 #pragma unroll
     for (int j = 0; j < 8; ++j)
-      store16<REV>(orsrc, ol, a.O.vec, j,
-                   pair_round<DT>(o[j >> 2][0][j & 3] * a.oscale, o[j >> 2][1][j & 3] * a.oscale));
+      if (now.width == 32 || takes(now, g, j))
+        store16<REV>(orsrc, ot, a.O.vec, j,
+                     pair_round<DT>(o[j >> 2][0][j & 3] * a.oscale, o[j >> 2][1][j & 3] * a.oscale));
+    c = next;
     __syncthreads();
   }
 
@@ -672,9 +723,14 @@ constexpr size_t scan_grad_lds() {
   return (size_t)2 * kScanC * (NV * 32 + kPadRow) * 2 + (size_t)NV * 32 * kTokRow * 2 + 64;
 }
 
-template <int DT, int NV, int NW, bool REV, bool GRAD>
-__global__ __launch_bounds__(NW * 64, 2) void scan_grad_kernel(const ScanArgs a) {
+template <int DT, bool G32, int NV, int NW, bool REV, bool GRAD>
+__global__ __launch_bounds__(NW * 64, NV > 4 ? 1 : 2) void scan_grad_kernel(const ScanArgs a) {
   constexpr int DVP = NV * 32, RS = DVP + kPadRow;
+  constexpr int gb = G32 ? 4 : 2;
+  constexpr int SL = (NV + NW - 1) / NW;        // slabs of 32 columns a wave stages
+  // terms of the state and the scores: two where everything is rounded to 16
+  // bits, three where the gates' gradient is kept in float32
+  constexpr int TP = G32 ? 3 : 2;
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
   uint16_t* vs = (uint16_t*)smem;               // V [32][RS]
   uint16_t* ws = vs + kScanC * RS;              // W [32][RS]
@@ -686,7 +742,6 @@ __global__ __launch_bounds__(NW * 64, 2) void scan_grad_kernel(const ScanArgs a)
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int n = lane & 15, g = lane >> 4;
   const int col = (p.blk * NW + wave) * 32 + 2 * n;       // the lane's channels col, col + 1
-  const int gb = a.g32 ? 4 : 2, gob = a.go32 ? 4 : 2;
   const int64_t head = (int64_t)p.seq * a.H + p.h;
   float* slot = a.slots ? a.slots + p.slot * (int64_t)a.dkp * a.dvp : nullptr;
 
@@ -719,7 +774,7 @@ __global__ __launch_bounds__(NW * 64, 2) void scan_grad_kernel(const ScanArgs a)
     xb = base_of(a.X, p, 2);
     wb = base_of(a.W, p, 2);
     ob = base_of(a.O, p, 2);
-    if (REV) dgb = base_of(a.DG, p, gob);
+    if (REV) dgb = base_of(a.DG, p, gb);
     // rows of all sequences in one run: (b t + token, h, dkp)
     qdq = a.qdq + ((p.b * a.t + p.row0) * a.H + p.h) * a.dkp;
     if (REV) {
@@ -729,195 +784,172 @@ __global__ __launch_bounds__(NW * 64, 2) void scan_grad_kernel(const ScanArgs a)
     }
   }
   const Lane kl = lane_of<REV>(a.K, g, col, a.dk, 2), gl = lane_of<REV>(a.G, g, col, a.dk, gb);
+  Lane xl = kl, ol = kl, dl = kl, wl[SL], vl[SL];
+  if (GRAD) {
+    xl = lane_of<REV>(a.X, g, col, a.dk, 2);
+    ol = lane_of<REV>(a.O, g, col, a.dk, 2);
+    if (REV) dl = lane_of<REV>(a.DG, g, col, a.dk, gb);
+  }
+#pragma unroll
+  for (int i = 0; i < SL; ++i) {
+    const int e0 = 32 * (wave + i * NW) + 2 * n;
+    vl[i] = lane_of<REV>(a.V, g, e0, a.dv, 2);
+    if (GRAD) wl[i] = lane_of<REV>(a.W, g, e0, a.dv, 2);
+  }
 
   const int nch = (int)((p.hi - p.lo + kScanC - 1) / kScanC);
-  for (int c = 0; c < nch; ++c) {
+  uint32_t kw[8], gw[kGateWords<G32>], vw[SL][8], ww[SL][8];
+  auto fetch = [&](int c) {
     const int64_t tok = p.lo + (int64_t)(REV ? nch - 1 - c : c) * kScanC;
     const int nv = (int)min((int64_t)kScanC, p.hi - tok);
-    uint32_t kw[8], gw[16], xw[8];
-    load_gates<REV>(chunk_rsrc(a.G, gbp, tok, nv, a.dk, gb), gl, a.G.vec, a.g32, gw);
+    const auto vr = chunk_rsrc(a.V, vb, tok, nv, a.dv, 2);
+#pragma unroll
+    for (int i = 0; i < SL; ++i) load16<REV>(vr, vl[i], a.V.vec, vw[i]);
+    if (GRAD) {
+      const auto wr = chunk_rsrc(a.W, wb, tok, nv, a.dv, 2);
+#pragma unroll
+      for (int i = 0; i < SL; ++i) load16<REV>(wr, wl[i], a.W.vec, ww[i]);
+    }
+    load_gates<REV, G32>(chunk_rsrc(a.G, gbp, tok, nv, a.dk, gb), gl, a.G.vec, gw);
     load16<REV>(chunk_rsrc(a.K, kb, tok, nv, a.dk, 2), kl, a.K.vec, kw);
-    if (GRAD) load16<REV>(chunk_rsrc(a.X, xb, tok, nv, a.dk, 2), lane_of<REV>(a.X, g, col, a.dk, 2), a.X.vec, xw);
-    bool wildv = false;
-    for (int s = wave; s < NV; s += NW) {
-      const int e0 = 32 * s + 2 * n;
-      uint32_t w[8];
-      load16<REV>(chunk_rsrc(a.V, vb, tok, nv, a.dv, 2), lane_of<REV>(a.V, g, e0, a.dv, 2), a.V.vec, w);
+  };
+  if (nch > 0) fetch(0);
+  Step st = {0, 32};
+  for (int c = 0; c < nch;) {
+    const int64_t tok = p.lo + (int64_t)(REV ? nch - 1 - c : c) * kScanC;
+    const int nv = (int)min((int64_t)kScanC, p.hi - tok);
+    bool hard = false;
+#pragma unroll
+    for (int i = 0; i < SL; ++i) {
+      const int s = wave + i * NW, e0 = 32 * s + 2 * n;
+      if (NV % NW != 0 && s >= NV) break;
+      uint32_t v[8];
+      take(st, g, vw[i], v);
       u32x4 c0, c1;
-      columns_of(w, c0, c1);
+      columns_of(v, c0, c1);
       *(u32x4*)(vt + e0 * kTokRow + 8 * g) = c0;
       *(u32x4*)(vt + (e0 + 1) * kTokRow + 8 * g) = c1;
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        wildv |= pair_wild<DT>(w[j]);
-        *(uint32_t*)(vs + (8 * g + j) * RS + e0) = w[j];
+        hard |= pair_wild<DT>(v[j]);
+        if (GRAD) *(uint32_t*)(vs + (8 * g + j) * RS + e0) = v[j];
       }
       if (GRAD) {
-        load16<REV>(chunk_rsrc(a.W, wb, tok, nv, a.dv, 2), lane_of<REV>(a.W, g, e0, a.dv, 2), a.W.vec, w);
+        take(st, g, ww[i], v);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          wildv |= pair_wild<DT>(w[j]);
-          *(uint32_t*)(ws + (8 * g + j) * RS + e0) = w[j];
+          hard |= pair_wild<DT>(v[j]);
+          *(uint32_t*)(ws + (8 * g + j) * RS + e0) = v[j];
         }
       }
     }
-    const bool anyv = __ballot(wildv) != 0;
-    if (lane == 0) wild[wave] = anyv;
-    float gv[2][8];
-    gate_values<DT>(gw, a.g32, gv);
     Gates q;
-    make_gates<REV>(gv, lane, q);
-    float kf[2][8];
-    uint32_t big = 0;
+    step_gates<DT, G32, REV>(st, gw, lane, q);
+    bf16x8 kk[2][3];
+    {
+      uint32_t kv[8], big = 0;
+      take(st, g, kw, kv);
+      float kf[2][8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      kf[0][j] = pair_lo<DT>(kw[j]) * a.kscale * q.down[0][j];
-      kf[1][j] = pair_hi<DT>(kw[j]) * a.kscale * q.down[1][j];
-      big = max(big, max(mag(kf[0][j]), mag(kf[1][j])));
-    }
-    gsum[0] += q.sum[0];
-    gsum[1] += q.sum[1];
-    int hard = __ballot(q.hard || big > kBigBits) != 0;
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < NW; ++w) hard |= wild[w];
-
-    f32x4 o[2][2] = {};
-    if (!__builtin_amdgcn_readfirstlane(hard)) {
-      bf16x8 kk[2][3];
+      for (int j = 0; j < 8; ++j) {
+        kf[0][j] = pair_lo<DT>(kv[j]) * a.kscale * q.down[0][j];
+        kf[1][j] = pair_hi<DT>(kv[j]) * a.kscale * q.down[1][j];
+        big = max(big, max(mag(kf[0][j]), mag(kf[1][j])));
+      }
+      hard |= q.hard || big > kBigBits;
       split8<3>(kf[0], kk[0]);
       split8<3>(kf[1], kk[1]);
-      if (GRAD) {
-        f32x4 pt[2][2] = {};   // W_i . V_j, rows j, columns i
+    }
+    const bool any = __ballot(hard) != 0;
+    if (lane == 0) wild[wave] = any;
+    __syncthreads();
+    int all = 0;
 #pragma unroll
-        for (int s = 0; s < NV; ++s) {
-          u32x4 vv[2], wr[2];
-          bf16x8 ww[2][kTerms<DT>];
-#pragma unroll
-          for (int tl = 0; tl < 2; ++tl) {
-            vv[tl] = *(const u32x4*)(vs + row_of(n, tl) * RS + 32 * s + 8 * g);
-            wr[tl] = *(const u32x4*)(ws + row_of(n, tl) * RS + 32 * s + 8 * g);
-            exact_terms<DT>(wr[tl], ww[tl]);
-          }
-#pragma unroll
-          for (int jt = 0; jt < 2; ++jt)
-#pragma unroll
-            for (int it = 0; it < 2; ++it) {
-              if constexpr (DT == DT_F16)
-                pt[jt][it] = mfma(__builtin_bit_cast(f16x8, vv[jt]), __builtin_bit_cast(f16x8, wr[it]), pt[jt][it]);
-              else
-                pt[jt][it] = mfma(__builtin_bit_cast(bf16x8, vv[jt]), ww[it][0], pt[jt][it]);
-            }
-#pragma unroll
-          for (int nt = 0; nt < 2; ++nt) {
-            float x[8];
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-              x[r] = S[s][0][nt][r] *= q.a[nt];
-              x[4 + r] = S[s][1][nt][r] *= q.a[nt];
-            }
-            bf16x8 st[3];
-            split8<3>(x, st);
-#pragma unroll
-            for (int it = 0; it < 2; ++it) o[it][nt] = mfma_terms(ww[it], st, o[it][nt]);
-          }
-        }
-#pragma unroll
-        for (int it = 0; it < 2; ++it) {
-          float x[8];
-#pragma unroll
-          for (int jt = 0; jt < 2; ++jt)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) x[4 * jt + r] = 8 * g + 4 * jt + r <= row_of(n, it) ? pt[jt][it][r] : 0.0f;
-          bf16x8 ps[3];
-          split8<3>(x, ps);
-#pragma unroll
-          for (int nt = 0; nt < 2; ++nt) o[it][nt] = mfma_terms(ps, kk[nt], o[it][nt]);
-        }
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-#pragma unroll
-          for (int nt = 0; nt < 2; ++nt) o[j >> 2][nt][j & 3] *= q.up[nt][j];
-      } else {
-#pragma unroll
-        for (int s = 0; s < NV; ++s)
-#pragma unroll
-          for (int tl = 0; tl < 2; ++tl)
-#pragma unroll
-            for (int nt = 0; nt < 2; ++nt) S[s][tl][nt] *= q.a[nt];
-      }
-#pragma unroll
-      for (int s = 0; s < NV; ++s)
-#pragma unroll
-        for (int tl = 0; tl < 2; ++tl) {
-          bf16x8 vv[kTerms<DT>];
-          exact_terms<DT>(*(const u32x4*)(vt + (32 * s + row_of(n, tl)) * kTokRow + 8 * g), vv);
-#pragma unroll
-          for (int nt = 0; nt < 2; ++nt) S[s][tl][nt] = mfma_terms(vv, kk[nt], S[s][tl][nt]) * q.b[nt];
-        }
-    } else {
-      for (int tg = 0; tg < 4; ++tg) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const uint32_t kraw = __shfl(kw[j], 16 * tg + n, 64);
-          const float k0 = pair_lo<DT>(kraw) * a.kscale, k1 = pair_hi<DT>(kraw) * a.kscale;
-          const float e0 = expf(__shfl(gv[0][j], 16 * tg + n, 64)), e1 = expf(__shfl(gv[1][j], 16 * tg + n, 64));
-          const uint16_t *vr = vs + (8 * tg + j) * RS, *wr = ws + (8 * tg + j) * RS;
-          float s0 = 0.0f, s1 = 0.0f;
-#pragma unroll
-          for (int s = 0; s < NV; ++s)
-#pragma unroll
-            for (int tl = 0; tl < 2; ++tl) {
-              const u32x2 v = *(const u32x2*)(vr + 32 * s + 8 * g + 4 * tl);
-              u32x2 w = {};
-              if (GRAD) w = *(const u32x2*)(wr + 32 * s + 8 * g + 4 * tl);
-#pragma unroll
-              for (int r = 0; r < 4; ++r) {
-                const uint32_t vw = v[r >> 1], ww = w[r >> 1];
-                const float vx = r & 1 ? pair_hi<DT>(vw) : pair_lo<DT>(vw);
-                float y0 = S[s][tl][0][r], y1 = S[s][tl][1][r];
-                if (!REV) {
-                  y0 *= e0;
-                  y1 *= e1;
-                }
-                y0 = __builtin_fmaf(k0, vx, y0);
-                y1 = __builtin_fmaf(k1, vx, y1);
-                if (GRAD) {
-                  const float wx = r & 1 ? pair_hi<DT>(ww) : pair_lo<DT>(ww);
-                  s0 = __builtin_fmaf(wx, y0, s0);
-                  s1 = __builtin_fmaf(wx, y1, s1);
-                }
-                if (REV) {
-                  y0 *= e0;
-                  y1 *= e1;
-                }
-                S[s][tl][0][r] = y0;
-                S[s][tl][1][r] = y1;
-              }
-            }
-          if (GRAD) {
-            s0 += __shfl_xor(s0, 16, 64);
-            s1 += __shfl_xor(s1, 16, 64);
-            s0 += __shfl_xor(s0, 32, 64);
-            s1 += __shfl_xor(s1, 32, 64);
-            if (g == tg) {
-              o[j >> 2][0][j & 3] = s0;
-              o[j >> 2][1][j & 3] = s1;
-            }
-          }
-        }
-      }
+    for (int w = 0; w < NW; ++w) all |= wild[w];
+    if (st.width > 1 && __builtin_amdgcn_readfirstlane(all)) {
+      smaller(st);
+      __syncthreads();
+      continue;
+    }
+
+    gsum[0] += q.sum[0];
+    gsum[1] += q.sum[1];
+    uint32_t xw[8];
+    if (GRAD) load16<REV>(chunk_rsrc(a.X, xb, tok, nv, a.dk, 2), xl, a.X.vec, xw);
+    const Step now = st;
+    advance(st);
+    const int next = st.pos == kScanC ? c + 1 : c;
+    if (next != c) {
+      st = Step{0, 32};
+      if (next < nch) fetch(next);   // in flight during the products
     }
     if (GRAD) {
+      f32x4 o[2][2] = {};
+      f32x4 pt[2][2] = {};   // W_i . V_j, rows j, columns i
+#pragma unroll
+      for (int s = 0; s < NV; ++s) {
+        u32x4 vv[2], wr[2];
+        bf16x8 wt[2][kTerms<DT>];
+#pragma unroll
+        for (int tl = 0; tl < 2; ++tl) {
+          vv[tl] = *(const u32x4*)(vs + row_of(n, tl) * RS + 32 * s + 8 * g);
+          wr[tl] = *(const u32x4*)(ws + row_of(n, tl) * RS + 32 * s + 8 * g);
+          exact_terms<DT>(wr[tl], wt[tl]);
+        }
+#pragma unroll
+        for (int jt = 0; jt < 2; ++jt)
+#pragma unroll
+          for (int it = 0; it < 2; ++it) {
+            if constexpr (DT == DT_F16)
+              pt[jt][it] = mfma(__builtin_bit_cast(f16x8, vv[jt]), __builtin_bit_cast(f16x8, wr[it]), pt[jt][it]);
+            else
+              pt[jt][it] = mfma(__builtin_bit_cast(bf16x8, vv[jt]), wt[it][0], pt[jt][it]);
+          }
+#pragma unroll
+        for (int nt = 0; nt < 2; ++nt) {
+          float x[8];
+          S[s][0][nt] *= q.a[nt];
+          S[s][1][nt] *= q.a[nt];
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            x[r] = S[s][0][nt][r];
+            x[4 + r] = S[s][1][nt][r];
+          }
+          bf16x8 sx[TP];
+          split8<TP>(x, sx);
+#pragma unroll
+          for (int it = 0; it < 2; ++it) o[it][nt] = mfma_terms(wt[it], sx, o[it][nt]);
+        }
+      }
+#pragma unroll
+      for (int it = 0; it < 2; ++it) {
+        float x[8];
+#pragma unroll
+        for (int jt = 0; jt < 2; ++jt)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) x[4 * jt + r] = 8 * g + 4 * jt + r <= row_of(n, it) ? pt[jt][it][r] : 0.0f;
+        bf16x8 ps[TP];
+        split8<TP>(x, ps);
+#pragma unroll
+        for (int nt = 0; nt < 2; ++nt) {
+          if constexpr (TP == 3) {
+            o[it][nt] = mfma_terms(ps, kk[nt], o[it][nt]);
+          } else {
+            const bf16x8 k2[2] = {kk[nt][0], kk[nt][1]};
+            o[it][nt] = mfma_terms(ps, k2, o[it][nt]);
+          }
+        }
+      }
       const __amdgpu_buffer_rsrc_t orsrc = chunk_rsrc(a.O, ob, tok, nv, a.dk, 2);
-      const Lane ol = lane_of<REV>(a.O, g, col, a.dk, 2);
+      const Lane ot = fresh(ol);
       float y[2][8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const float o0 = o[j >> 2][0][j & 3] * a.oscale, o1 = o[j >> 2][1][j & 3] * a.oscale;
-        store16<REV>(orsrc, ol, a.O.vec, j, pair_round<DT>(o0, o1));
-        y[0][j] = pair_lo<DT>(xw[j]) * o0;
-        y[1][j] = pair_hi<DT>(xw[j]) * o1;
+        const float o0 = o[j >> 2][0][j & 3] * q.up[0][j] * a.oscale, o1 = o[j >> 2][1][j & 3] * q.up[1][j] * a.oscale;
+        const bool mine = now.width == 32 || takes(now, g, j);
+        if (mine) store16<REV>(orsrc, ot, a.O.vec, j, pair_round<DT>(o0, o1));
+        y[0][j] = mine ? pair_lo<DT>(xw[j]) * o0 : 0.0f;
+        y[1][j] = mine ? pair_hi<DT>(xw[j]) * o1 : 0.0f;
       }
       // the workspace's rows of this chunk: the lane's tokens are rows of H dkp floats
       float* qr = qdq + tok * a.H * a.dkp + col;
@@ -926,24 +958,25 @@ __global__ __launch_bounds__(NW * 64, 2) void scan_grad_kernel(const ScanArgs a)
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           const int i = 8 * g + j;
-          if (i < nv && col < a.dkp) *(f32x2*)(qr + i * qs) = f32x2{y[0][j], y[1][j]};
+          if ((now.width == 32 || takes(now, g, j)) && i < nv && col < a.dkp)
+            *(f32x2*)(qr + i * qs) = f32x2{y[0][j], y[1][j]};
         }
       } else {
-        // dg_t = (the value behind the chunk) + sum over this and the later tokens of q dq - k dk
+        // dg_t = (the value behind the step) + sum over this and the later tokens of q dq - k dk
         float run[2] = {0.0f, 0.0f}, d[2][8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           const int i = 31 - 8 * g - j;
           f32x2 u = {0.0f, 0.0f};
-          if (i < nv && col < a.dkp) u = *(const f32x2*)(qr + i * qs);
+          if ((now.width == 32 || takes(now, g, j)) && i < nv && col < a.dkp) u = *(const f32x2*)(qr + i * qs);
 #pragma unroll
           for (int nt = 0; nt < 2; ++nt) {
             run[nt] += u[nt] - y[nt][j];
             d[nt][j] = run[nt];
           }
         }
-        const __amdgpu_buffer_rsrc_t drsrc = chunk_rsrc(a.DG, dgb, tok, nv, a.dk, gob);
-        const Lane dl = lane_of<REV>(a.DG, g, col, a.dk, gob);
+        const __amdgpu_buffer_rsrc_t drsrc = chunk_rsrc(a.DG, dgb, tok, nv, a.dk, gb);
+        const Lane dt = fresh(dl);
 #pragma unroll
         for (int nt = 0; nt < 2; ++nt) {
           float s = run[nt];
@@ -959,17 +992,35 @@ __global__ __launch_bounds__(NW * 64, 2) void scan_grad_kernel(const ScanArgs a)
         }
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          if (a.go32) {
+          if (!(now.width == 32 || takes(now, g, j))) continue;
+          if constexpr (G32) {
             __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, d[0][j]), drsrc,
-                                                  dl.off0 + tok_off<REV>(dl, j), 0, 0);
+                                                  dt.off0 + tok_off<REV>(dt, j), 0, 0);
             __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, d[1][j]), drsrc,
-                                                  dl.off1 + tok_off<REV>(dl, j), 0, 0);
+                                                  off1_of<4>(dt) + tok_off<REV>(dt, j), 0, 0);
           } else {
-            store16<REV>(drsrc, dl, a.DG.vec, j, pair_round<DT>(d[0][j], d[1][j]));
+            store16<REV>(drsrc, dt, a.DG.vec, j, pair_round<DT>(d[0][j], d[1][j]));
           }
         }
       }
+    } else {
+#pragma unroll
+      for (int s = 0; s < NV; ++s)
+#pragma unroll
+        for (int tl = 0; tl < 2; ++tl)
+#pragma unroll
+          for (int nt = 0; nt < 2; ++nt) S[s][tl][nt] *= q.a[nt];
     }
+#pragma unroll
+    for (int s = 0; s < NV; ++s)
+#pragma unroll
+      for (int tl = 0; tl < 2; ++tl) {
+        bf16x8 vv[kTerms<DT>];
+        exact_terms<DT>(*(const u32x4*)(vt + (32 * s + row_of(n, tl)) * kTokRow + 8 * g), vv);
+#pragma unroll
+        for (int nt = 0; nt < 2; ++nt) S[s][tl][nt] = mfma_terms(vv, kk[nt], S[s][tl][nt]) * q.b[nt];
+      }
+    c = next;
     __syncthreads();
   }
 

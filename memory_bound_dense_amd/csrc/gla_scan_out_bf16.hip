@@ -1,0 +1,10 @@
+// libgemv.so, continued: the bf16 forms of scan_out_kernel.
+#include "gla_scan_table.h"
+
+namespace mbd {
+
+#define FORM(G32, N, REV) {&scan_out_kernel<DT_BF16, G32, N, 2, REV>, &scan_out_kernel<DT_BF16, G32, N, 4, REV>}
+#define FORMS(G32, REV) {FORM(G32, 2, REV), FORM(G32, 4, REV), FORM(G32, 8, REV)}
+extern const ScanForms kScanOutBf16 = {{FORMS(false, false), FORMS(false, true)}, {FORMS(true, false), FORMS(true, true)}};
+
+}  // namespace mbd

@@ -1,5 +1,6 @@
-// The compiled forms of the scan kernels, each table in a source file of its
-// own: [dtype][reversed][64, 128 or 256 channels][2 or 4 waves].
+// The compiled forms of the scan kernels, the table of each kernel and dtype in
+// a source file of its own: [float32 gates][reversed][64, 128 or 256 channels]
+// [2 or 4 waves].
 #pragma once
 
 #include "gla_scan_kernel.h"
@@ -7,8 +8,9 @@
 namespace mbd {
 
 using ScanFn = void (*)(const ScanArgs);
-extern const ScanFn kScanOut[2][2][3][2];     // channels: DK
-extern const ScanFn kScanGrad[2][2][3][2];    // channels: DV
-extern const ScanFn kScanState[2][2][3][2];   // channels: DV
+using ScanForms = ScanFn[2][2][3][2];
+extern const ScanForms kScanOutF16, kScanOutBf16;       // channels: DK
+extern const ScanForms kScanGradF16, kScanGradBf16;     // channels: DV
+extern const ScanForms kScanStateF16, kScanStateBf16;   // channels: DV
 
 }  // namespace mbd

@@ -104,8 +104,10 @@ def check_bwd(x, r, seq, rows, out=0):
     t, g = a[0].shape[0], a[3]
     for n in ("dq", "dk", "dv"):
         close(n, r[n][seq, rows], want[n], scan_ref.rel16(t, g) * ab[n], x["q"].dtype)
-    # q dq - k dk with both in three terms: the bound of a float32 result on each term
-    close("dg", r["dg"][seq, rows], want["dg"], 2 * scan_ref.rel32(t, g) * ab["dg_run"], x["g"].dtype)
+    # a sum of q dq - k dk: with float32 gates both come from three-term factors (the bound of
+    # a float32 result on each term), with 16-bit gates from two-term ones
+    rel = scan_ref.rel32(t, g) if x["g"].dtype == F32 else scan_ref.rel16(t, g)
+    close("dg", r["dg"][seq, rows], want["dg"], 2 * rel * ab["dg_run"], x["g"].dtype)
     close("dS0", r["dS0"][out], want["dS0"], scan_ref.rel32(t, g) * ab["dS0"], F32)
 
 
@@ -133,3 +135,71 @@ def test_backward(scan, b, t, h, dk, dv, dt, gt):
     r = bwd(scan, x)
     for s in range(b):
         check_bwd(x, r, s, slice(None), s)
+
+
+# Gates that do not fit a chunk of products: steps of 8 tokens (a sum of 40 over half a chunk),
+# of one token (a gate beyond 80, -inf), and both next to ordinary chunks.
+
+def hard_gates(x, kind):
+    g = x["g"]
+    t = g.shape[1]
+    gen = torch.Generator().manual_seed(t)
+    if kind == "strong":
+        g[:] = -3.0 - torch.rand(g.shape, generator=gen) * 2
+    elif kind == "spikes":          # single gates of -60, -100 and -inf
+        for i, v in enumerate((-60.0, -100.0, -float("inf"), -1e30)):
+            g[:, (11 + 37 * i) % t, :, i::5] = v
+    elif kind == "reset":           # the state cleared as a whole, more than once
+        g[:, t // 3] = -float("inf")
+        g[:, (2 * t) // 3:(2 * t) // 3 + 2] = -float("inf")
+    elif kind == "growing":
+        g[:] = torch.rand(g.shape, generator=gen) * 0.2
+        g[:, ::7] = -1.5
+    return x
+
+
+@pytest.mark.parametrize("kind", ["strong", "spikes", "reset", "growing"])
+@pytest.mark.parametrize("t,dk,dv", [(70, 64, 64), (130, 128, 96), (300, 40, 256)])
+@pytest.mark.parametrize("dt,gt", TYPES, ids=TIDS)
+def test_gates_of_every_size(scan, kind, t, dk, dv, dt, gt):
+    x = hard_gates(inputs(1, t, 2, dk, dv, dt, gt, gate=4.0), kind)
+    o, ST = fwd(scan, x)
+    check_fwd(x, o, ST, 0, slice(None))
+    check_bwd(x, bwd(scan, x), 0, slice(None))
+
+
+@pytest.mark.parametrize("what", ["q", "k", "v", "do", "g"])
+@pytest.mark.parametrize("value", [float("nan"), float("inf")], ids=["nan", "inf"])
+@pytest.mark.parametrize("t", [90, 300])
+def test_nothing_leaks_from_other_tokens(scan, what, value, t):
+    """A token with a NaN or infinity: no result that does not depend on it changes a bit
+    (earlier tokens' o, later tokens' dk and dv, every other head), and those that do are
+    not finite."""
+    x = inputs(1, t, 2, 64, 64, BF, BF, gate=16.0, state=False)
+    at = t // 2 + 3
+    clean_o, clean_S = fwd(scan, x)
+    clean = bwd(scan, x)
+    x[what][0, at, 0, 5] = value
+    o, ST = fwd(scan, x)
+    r = bwd(scan, x)
+    assert torch.equal(o[:, :, 1], clean_o[:, :, 1])
+    for n in ("dq", "dk", "dv", "dg"):
+        assert torch.equal(r[n][:, :, 1], clean[n][:, :, 1]), n
+    assert torch.equal(ST[:, 1], clean_S[:, 1])
+    e = U * 2 ** 12      # chunk boundaries may fall into other steps: only rounding may differ
+    near = lambda a, b: torch.allclose(a.float(), b.float(), rtol=2 ** -7, atol=e)
+    if what != "do":
+        assert near(o[0, :at, 0], clean_o[0, :at, 0])
+    if what == "q":
+        assert not torch.isfinite(o[0, at, 0]).any() and near(o[0, at + 1:, 0], clean_o[0, at + 1:, 0])
+        assert torch.isfinite(ST).all()
+    if what in ("k", "v"):
+        assert not torch.isfinite(ST[0, 0]).all()
+        # dk and dv of later tokens do not depend on this token's k, v
+        assert near(r["dk"][0, at + 1:, 0], clean["dk"][0, at + 1:, 0])
+        assert near(r["dv"][0, at + 1:, 0], clean["dv"][0, at + 1:, 0])
+        assert near(r["dq"][0, :at, 0], clean["dq"][0, :at, 0])
+    if what in ("q", "do"):
+        assert near(r["dk"][0, at + 1:, 0], clean["dk"][0, at + 1:, 0])
+        assert near(r["dv"][0, at + 1:, 0], clean["dv"][0, at + 1:, 0])
+        assert not torch.isfinite(r["dk" if what == "do" else "dv"][0, at, 0]).all()
