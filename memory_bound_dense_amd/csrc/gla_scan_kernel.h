@@ -57,7 +57,7 @@ typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
 constexpr int kScanC = 32;               // tokens per chunk
 constexpr float kRange = 40.0f;          // largest |G - r| of a chunk done as products
-constexpr uint32_t kBigBits = 0x7cf0bdc2u;   // 1e37f: larger factors (and NaN) are left to the recurrence
+constexpr float kBig = 1e37f;            // chunks with larger factors are done token by token
 
 // A (sequence, token, head, channel) tensor: element strides, channels dense.
 struct ScanTensor {
@@ -282,74 +282,74 @@ struct Gates {
   float sum[2];       // end
   bool hard;
 };
-// Gates are summed as whole multiples of 2^-24 in units of log 2: exact sums,
-// each gate within 2^-25, and an exponential is a table-free 2^fraction scaled
-// by the whole part.  Summed in fp32, chunks of strong gates lose up to 2^-24
-// |G| (1e-6 at |G| = 20) in every decay.
-constexpr float kFix = 16777216.0f * 1.44269504f;
-constexpr int32_t kFixRange = (int32_t)(kRange * kFix);        // |G - r| (at most 88.7: 31 bits)
-constexpr int32_t kFixSum = 2100000000;                        // |G|: sums that reach it may have saturated
-__device__ __forceinline__ int32_t add_sat(int32_t a, int32_t b) { return __builtin_elementwise_add_sat(a, b); }
-__device__ __forceinline__ int32_t abs_of(int32_t x) { return max(x, -x); }
-// 2^(d / 2^24) and its reciprocal
-__device__ __forceinline__ void exp_pair(int32_t d, float& up, float& down) {
-  const int32_t whole = d >> 24;
-  const float p = __builtin_amdgcn_exp2f((float)(d & 0xffffff) * 5.9604644775390625e-8f);
-  up = __builtin_amdgcn_ldexpf(p, whole);
-  down = __builtin_amdgcn_ldexpf(__builtin_amdgcn_rcpf(p), -whole);
+// Gates are summed as whole multiples of 2^-25 in units of log 2: exact sums
+// (modulo 2^32, which leaves differences within the range right), each gate
+// within 2^-25, and an exponential is 2^fraction scaled by the whole part.
+// Summed in fp32, chunks of strong gates lose up to 2^-24 |G| (1e-6 at |G| =
+// 20) in every decay, and a correctly rounded e^x costs more instructions.
+constexpr float kFix = 33554432.0f * 1.44269504f;
+static_assert(kRange * 1.4427f < 63.0f, "G - r as a multiple of 2^-25 has to fit 32 bits");
+// 2^(d / 2^25 + 1) / 2 in two factors: 2^(1 + fraction) in [2, 4) and a power of two.
+__device__ __forceinline__ float fraction_exp(int32_t d) {
+  return __builtin_amdgcn_exp2f(__builtin_bit_cast(float, (((uint32_t)d >> 2) & 0x7fffffu) | 0x3f800000u));
 }
-__device__ __forceinline__ float exp_fix(int32_t d) {
-  return __builtin_amdgcn_ldexpf(__builtin_amdgcn_exp2f((float)(d & 0xffffff) * 5.9604644775390625e-8f), d >> 24);
-}
-template <int DT, bool G32, bool REV, bool UP = true>
+__device__ __forceinline__ float exp_fix(int32_t d) { return __builtin_amdgcn_ldexpf(fraction_exp(d), (d >> 25) - 1); }
+template <int DT, bool G32, bool REV>
 __device__ __forceinline__ void make_gates(const uint32_t (&w)[kGateWords<G32>], int lane, Gates& q) {
   const int g = lane >> 4;
-  uint32_t wild = 0;
-  int32_t far = 0, sum = 0;
+  float total = 0.0f;
 #pragma unroll
   for (int c = 0; c < 2; ++c) {
     int32_t run = 0, G[8];
+    float size = 0.0f;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const float x = gate_value<DT, G32>(w, c, j);
-      wild = max(wild, __builtin_bit_cast(uint32_t, x) & 0x7fffffffu);
+      size += __builtin_fabsf(x);
       if (REV) G[j] = run;
-      run = add_sat(run, (int32_t)__builtin_rintf(x * kFix));   // the conversion saturates
+      run += (int32_t)(x * kFix);
       if (!REV) G[j] = run;
     }
+    total = __builtin_fmaxf(total, size);
+    if (!(size <= kRange)) total = __builtin_inff();   // NaN too
     int32_t a = run;
     const int32_t u = __shfl_up(a, 16, 64);
-    if (g >= 1) a = add_sat(a, u);
+    if (g >= 1) a += u;
     const int32_t v = __shfl_up(a, 32, 64);
-    if (g >= 2) a = add_sat(a, v);
-    const int32_t before = __shfl_up(a, 16, 64);
+    if (g >= 2) a += v;
     const int32_t mid = __shfl(a, 16 + (lane & 15), 64);
     const int32_t end = __shfl(a, 48 + (lane & 15), 64);
-    const int32_t base = g >= 1 ? before : 0;
-    sum = max(sum, max(abs_of(a), abs_of(end)));
+    const int32_t base = a - run - mid;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const int32_t x = add_sat(base, G[j]);
-      const int32_t d = __builtin_elementwise_sub_sat(x, mid);
-      sum = max(sum, abs_of(x));
-      far = max(far, abs_of(d));
-      exp_pair(d, q.up[c][j], q.down[c][j]);
+      const int32_t d = base + G[j], whole = d >> 25;
+      const float p = fraction_exp(d);
+      q.up[c][j] = __builtin_amdgcn_ldexpf(p, whole - 1);
+      q.down[c][j] = __builtin_amdgcn_ldexpf(__builtin_amdgcn_rcpf(p), 1 - whole);
     }
-    far = max(far, max(mid, __builtin_elementwise_sub_sat(end, mid)));
     q.a[c] = exp_fix(mid);
-    q.b[c] = exp_fix(__builtin_elementwise_sub_sat(end, mid));
-    q.sum[c] = (float)end * (1.0f / kFix);
+    q.b[c] = exp_fix(end - mid);
+    q.sum[c] = ((float)mid + (float)(end - mid)) * (1.0f / kFix);
   }
-  // NaN and gates beyond 80 (their fixed-point form has saturated) in `wild`
-  q.hard = wild > 0x42a00000u || far > kFixRange || sum > kFixSum;
+  // |G - r| <= the sum of |g| over one half of the chunk (two lane groups)
+  total += __shfl_xor(total, 16, 64);
+  q.hard = !(total <= kRange);
 }
 
-__device__ __forceinline__ uint32_t mag(float x) { return __builtin_bit_cast(uint32_t, x) & 0x7fffffffu; }
-// Whether a pair of 16-bit values holds one that is not finite.
+typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+// The larger magnitudes of two pairs of 16-bit values, by their bits (NaN the
+// largest), and whether a pair holds one that is not finite.
+__device__ __forceinline__ uint32_t pair_max(uint32_t m, uint32_t w) {
+  return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2, m),
+                                                                __builtin_bit_cast(u16x2, w & 0x7fff7fffu)));
+}
 template <int DT>
-__device__ __forceinline__ bool pair_wild(uint32_t w) {
+__device__ __forceinline__ bool pair_wild(uint32_t m) {
   constexpr uint32_t e = DT == DT_F16 ? 0x7c00u : 0x7f80u;
-  return (w & e) == e || ((w >> 16) & e) == e;
+  return (m & 0xffffu) >= e || (m >> 16) >= e;
+}
+__device__ __forceinline__ float max3(float m, float a, float b) {
+  return __builtin_fmaxf(__builtin_fmaxf(m, __builtin_fabsf(a)), __builtin_fabsf(b));
 }
 
 // Two channels' columns (token-major pairs) as channel-major operands.
@@ -477,7 +477,7 @@ __device__ __forceinline__ void step_gates(const Step& t, const uint32_t (&gw)[k
 template <int NS>
 constexpr size_t scan_out_lds() {
   return (size_t)4 * kScanC * (NS * 32 + kPadRow) * 2 + (size_t)3 * NS * 32 * kTokRow * 2 +
-         (size_t)2 * NS * 32 * 4 + 64;
+         (size_t)NS * 32 * 4 + 64;
 }
 
 template <int DT, bool G32, int NS, int NW, bool REV>
@@ -489,8 +489,8 @@ __global__ __launch_bounds__(NW * 64, NS > 4 ? 1 : 2) void scan_out_kernel(const
   uint16_t* xs = (uint16_t*)smem;                     // X e^{G-r}: 2 terms of [32][RS]
   uint16_t* ks = xs + 2 * kScanC * RS;                // K e^{r-G}: 2 terms of [32][RS]
   uint16_t* kt = ks + 2 * kScanC * RS;                // the same, 3 terms of [DKP][kTokRow]
-  float* dec = (float*)(kt + 3 * DKP * kTokRow);      // e^{r} [DKP], e^{end-r} [DKP]
-  int* wild = (int*)(dec + 2 * DKP);                  // one flag per wave
+  float* dec = (float*)(kt + 3 * DKP * kTokRow);      // the state's decay before the step, [DKP]
+  int* wild = (int*)(dec + DKP);                  // one flag per wave
 
   Place p;
   if (!place_of(a, p)) return;
@@ -556,6 +556,11 @@ __global__ __launch_bounds__(NW * 64, NS > 4 ? 1 : 2) void scan_out_kernel(const
     load16<REV>(chunk_rsrc(a.V, vb, tok, nv, a.dv, 2), vl, a.V.vec, vw);
   };
   if (nch > 0) fetch(0);
+  // a step's second half e^{end-r} is left to the next step, which scales the
+  // state by both at once
+  float left[SL][2], half[SL][2];
+#pragma unroll
+  for (int i = 0; i < SL; ++i) left[i][0] = left[i][1] = half[i][0] = half[i][1] = 1.0f;
   Step st = {0, 32};
   for (int c = 0; c < nch;) {
     const int64_t tok = p.lo + (int64_t)(REV ? nch - 1 - c : c) * kScanC;
@@ -567,43 +572,51 @@ __global__ __launch_bounds__(NW * 64, NS > 4 ? 1 : 2) void scan_out_kernel(const
       if (NS % NW != 0 && s >= NS) break;
       Gates q;
       step_gates<DT, G32, REV>(st, gw[i], lane, q);
-      uint32_t xt[8], kv[8];
+      uint32_t xt[8], kv[8], raw = 0, kt3[3][8];
       take(st, g, xw[i], xt);
       take(st, g, kw[i], kv);
-      float kf[2][8];
-      uint32_t big = 0;
+      float big = 0.0f;
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const int row = 8 * g + j;
+        raw = pair_max(pair_max(raw, xt[j]), kv[j]);
         const float x0 = pair_lo<DT>(xt[j]) * q.up[0][j], x1 = pair_hi<DT>(xt[j]) * q.up[1][j];
-        kf[0][j] = pair_lo<DT>(kv[j]) * a.kscale * q.down[0][j];
-        kf[1][j] = pair_hi<DT>(kv[j]) * a.kscale * q.down[1][j];
-        big = max(max(big, max(mag(x0), mag(x1))), max(mag(kf[0][j]), mag(kf[1][j])));
-        uint32_t t[2];
+        float k0 = pair_lo<DT>(kv[j]) * q.down[0][j], k1 = pair_hi<DT>(kv[j]) * q.down[1][j];
+        if (REV) {
+          k0 *= a.kscale;
+          k1 *= a.kscale;
+        }
+        big = max3(max3(big, x0, x1), k0, k1);
+        uint32_t t[2], u[3];
         split2<2>(x0, x1, t);
         *(uint32_t*)(xs + row * RS + d0) = t[0];
         *(uint32_t*)(xs + (kScanC + row) * RS + d0) = t[1];
-        split2<2>(kf[0][j], kf[1][j], t);
-        *(uint32_t*)(ks + row * RS + d0) = t[0];
-        *(uint32_t*)(ks + (kScanC + row) * RS + d0) = t[1];
+        split2<3>(k0, k1, u);
+        *(uint32_t*)(ks + row * RS + d0) = u[0];
+        *(uint32_t*)(ks + (kScanC + row) * RS + d0) = u[1];
+#pragma unroll
+        for (int m = 0; m < 3; ++m) kt3[m][j] = u[m];
       }
 #pragma unroll
-      for (int nt = 0; nt < 2; ++nt) {
-        bf16x8 t[3];
-        split8<3>(kf[nt], t);
-#pragma unroll
-        for (int m = 0; m < 3; ++m) *(bf16x8*)(kt + (m * DKP + d0 + nt) * kTokRow + 8 * g) = t[m];
-        if (g == 0) {
-          dec[d0 + nt] = q.a[nt];
-          dec[DKP + d0 + nt] = q.b[nt];
-        }
+      for (int m = 0; m < 3; ++m) {
+        u32x4 c0, c1;
+        columns_of(kt3[m], c0, c1);
+        *(u32x4*)(kt + (m * DKP + d0) * kTokRow + 8 * g) = c0;
+        *(u32x4*)(kt + (m * DKP + d0 + 1) * kTokRow + 8 * g) = c1;
       }
-      hard |= q.hard || big > kBigBits;
+      if (g == 0) {
+        // what the step before leaves to be done, and this step's first half
+        *(f32x2*)(dec + d0) = f32x2{q.a[0] * left[i][0], q.a[1] * left[i][1]};
+      }
+      half[i][0] = q.b[0];
+      half[i][1] = q.b[1];
+      hard |= q.hard || !(big <= kBig) || pair_wild<DT>(raw);
     }
-    uint32_t vv[8];
+    uint32_t vv[8], rawv = 0;
     take(st, g, vw, vv);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) hard |= pair_wild<DT>(vv[j]);
+    for (int j = 0; j < 8; ++j) rawv = pair_max(rawv, vv[j]);
+    hard |= pair_wild<DT>(rawv);
     const bool any = __ballot(hard) != 0;
     if (lane == 0) wild[wave] = any;
     __syncthreads();
@@ -616,6 +629,11 @@ __global__ __launch_bounds__(NW * 64, NS > 4 ? 1 : 2) void scan_out_kernel(const
       continue;
     }
 
+#pragma unroll
+    for (int i = 0; i < SL; ++i) {
+      left[i][0] = half[i][0];
+      left[i][1] = half[i][1];
+    }
     u32x4 vc[2];
     columns_of(vv, vc[0], vc[1]);
     const Step now = st;
@@ -681,9 +699,8 @@ __global__ __launch_bounds__(NW * 64, NS > 4 ? 1 : 2) void scan_out_kernel(const
 #pragma unroll
         for (int i = 0; i < 3; ++i)
           kk[i] = *(const bf16x8*)(kt + (i * DKP + 32 * s + row_of(n, tl)) * kTokRow + 8 * g);
-        const f32x4 d = *(const f32x4*)(dec + DKP + 32 * s + 8 * g + 4 * tl);
 #pragma unroll
-        for (int nt = 0; nt < 2; ++nt) S[s][tl][nt] = mfma_terms(kk, vt[nt], S[s][tl][nt]) * d;
+        for (int nt = 0; nt < 2; ++nt) S[s][tl][nt] = mfma_terms(kk, vt[nt], S[s][tl][nt]);
       }
     const __amdgpu_buffer_rsrc_t orsrc = chunk_rsrc(a.O, ob, tok, nv, a.dv, 2);
     const Lane ot = fresh(ol);
@@ -697,6 +714,14 @@ __global__ __launch_bounds__(NW * 64, NS > 4 ? 1 : 2) void scan_out_kernel(const
   }
 
   if (a.ST && (REV ? p.seg == 0 : p.last)) {
+    // the last step's second half
+#pragma unroll
+    for (int i = 0; i < SL; ++i) {
+      const int s = wave + i * NW;
+      if (NS % NW != 0 && s >= NS) break;
+      if (g == 0) *(f32x2*)(dec + 32 * s + 2 * n) = f32x2{left[i][0], left[i][1]};
+    }
+    __syncthreads();
 #pragma unroll
     for (int s = 0; s < NS; ++s)
 #pragma unroll
@@ -707,7 +732,7 @@ __global__ __launch_bounds__(NW * 64, NS > 4 ? 1 : 2) void scan_out_kernel(const
           for (int nt = 0; nt < 2; ++nt) {
             const int d = 32 * s + 8 * g + 4 * tl + r;
             if (d < a.dk && col + nt < vwidth)
-              a.ST[(((int64_t)p.seq * a.H + p.h) * a.dk + d) * a.dv + col + nt] = S[s][tl][nt][r];
+              a.ST[(((int64_t)p.seq * a.H + p.h) * a.dk + d) * a.dv + col + nt] = S[s][tl][nt][r] * dec[d];
           }
   }
 }
@@ -814,6 +839,7 @@ __global__ __launch_bounds__(NW * 64, NV > 4 ? 1 : 2) void scan_grad_kernel(cons
     load16<REV>(chunk_rsrc(a.K, kb, tok, nv, a.dk, 2), kl, a.K.vec, kw);
   };
   if (nch > 0) fetch(0);
+  float left[2] = {1.0f, 1.0f};   // a step's second half e^{end-r}, done with the next step's first
   Step st = {0, 32};
   for (int c = 0; c < nch;) {
     const int64_t tok = p.lo + (int64_t)(REV ? nch - 1 - c : c) * kScanC;
@@ -823,7 +849,7 @@ __global__ __launch_bounds__(NW * 64, NV > 4 ? 1 : 2) void scan_grad_kernel(cons
     for (int i = 0; i < SL; ++i) {
       const int s = wave + i * NW, e0 = 32 * s + 2 * n;
       if (NV % NW != 0 && s >= NV) break;
-      uint32_t v[8];
+      uint32_t v[8], raw = 0;
       take(st, g, vw[i], v);
       u32x4 c0, c1;
       columns_of(v, c0, c1);
@@ -831,32 +857,39 @@ __global__ __launch_bounds__(NW * 64, NV > 4 ? 1 : 2) void scan_grad_kernel(cons
       *(u32x4*)(vt + (e0 + 1) * kTokRow + 8 * g) = c1;
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        hard |= pair_wild<DT>(v[j]);
+        raw = pair_max(raw, v[j]);
         if (GRAD) *(uint32_t*)(vs + (8 * g + j) * RS + e0) = v[j];
       }
       if (GRAD) {
         take(st, g, ww[i], v);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          hard |= pair_wild<DT>(v[j]);
+          raw = pair_max(raw, v[j]);
           *(uint32_t*)(ws + (8 * g + j) * RS + e0) = v[j];
         }
       }
+      hard |= pair_wild<DT>(raw);
     }
     Gates q;
     step_gates<DT, G32, REV>(st, gw, lane, q);
     bf16x8 kk[2][3];
     {
-      uint32_t kv[8], big = 0;
+      uint32_t kv[8], raw = 0;
+      float big = 0.0f;
       take(st, g, kw, kv);
       float kf[2][8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        kf[0][j] = pair_lo<DT>(kv[j]) * a.kscale * q.down[0][j];
-        kf[1][j] = pair_hi<DT>(kv[j]) * a.kscale * q.down[1][j];
-        big = max(big, max(mag(kf[0][j]), mag(kf[1][j])));
+        raw = pair_max(raw, kv[j]);
+        kf[0][j] = pair_lo<DT>(kv[j]) * q.down[0][j];
+        kf[1][j] = pair_hi<DT>(kv[j]) * q.down[1][j];
+        if (REV) {
+          kf[0][j] *= a.kscale;
+          kf[1][j] *= a.kscale;
+        }
+        big = max3(big, kf[0][j], kf[1][j]);
       }
-      hard |= q.hard || big > kBigBits;
+      hard |= q.hard || !(big <= kBig) || pair_wild<DT>(raw);
       split8<3>(kf[0], kk[0]);
       split8<3>(kf[1], kk[1]);
     }
@@ -874,6 +907,11 @@ __global__ __launch_bounds__(NW * 64, NV > 4 ? 1 : 2) void scan_grad_kernel(cons
 
     gsum[0] += q.sum[0];
     gsum[1] += q.sum[1];
+#pragma unroll
+    for (int nt = 0; nt < 2; ++nt) {
+      q.a[nt] *= left[nt];
+      left[nt] = q.b[nt];
+    }
     uint32_t xw[8];
     if (GRAD) load16<REV>(chunk_rsrc(a.X, xb, tok, nv, a.dk, 2), xl, a.X.vec, xw);
     const Step now = st;
@@ -1018,12 +1056,19 @@ __global__ __launch_bounds__(NW * 64, NV > 4 ? 1 : 2) void scan_grad_kernel(cons
         bf16x8 vv[kTerms<DT>];
         exact_terms<DT>(*(const u32x4*)(vt + (32 * s + row_of(n, tl)) * kTokRow + 8 * g), vv);
 #pragma unroll
-        for (int nt = 0; nt < 2; ++nt) S[s][tl][nt] = mfma_terms(vv, kk[nt], S[s][tl][nt]) * q.b[nt];
+        for (int nt = 0; nt < 2; ++nt) S[s][tl][nt] = mfma_terms(vv, kk[nt], S[s][tl][nt]);
       }
     c = next;
     __syncthreads();
   }
 
+  // the last step's second half
+#pragma unroll
+  for (int s = 0; s < NV; ++s)
+#pragma unroll
+    for (int tl = 0; tl < 2; ++tl)
+#pragma unroll
+      for (int nt = 0; nt < 2; ++nt) S[s][tl][nt] *= left[nt];
   if (!GRAD) {
     // this segment's own state, from zero
 #pragma unroll
