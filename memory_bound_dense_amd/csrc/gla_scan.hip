@@ -14,7 +14,7 @@ namespace mbd {
 // state: one thread per 4 elements walks the sequence's segments.
 struct JoinArgs {
   float* slots;
-  const float* sums;
+  const float* decays;
   const float* S0;          // user layout, or null
   const int32_t* offsets;
   int64_t total, t;
@@ -41,13 +41,13 @@ __global__ __launch_bounds__(256) void scan_join_kernel(const JoinArgs a) {
   }
   const int64_t size = (int64_t)a.dkp * a.dvp;
   float* slot = a.slots + head * a.nseg * size + (int64_t)d * a.dvp + e;
-  const float* sum = a.sums + head * a.nseg * a.dkp + d;
+  const float* decay = a.decays + head * a.nseg * a.dkp + d;
 #pragma unroll 4
   for (int s = 0; s < ns; ++s) {
     const int64_t at = a.rev ? ns - 1 - s : s;
     f32x4* to = (f32x4*)(slot + at * size);
     const f32x4 u = *to;
-    const float f = expf(sum[at * a.dkp]);
+    const float f = decay[at * a.dkp];
     *to = x;
     x = x * f + u;
   }
@@ -72,7 +72,7 @@ struct ScanPlan {
   int nseg, L;
   int32_t dkp, dvp;
   int64_t heads;            // sequences x heads
-  size_t slots, slots2, sums, sums2, ends, qdq, bytes;
+  size_t slots, slots2, decays, decays2, ends, qdq, bytes;
 };
 
 int64_t up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
@@ -108,10 +108,10 @@ ScanPlan scan_plan(const gla_scan_t* p, bool backward) {
   const size_t states = (size_t)s.heads * s.nseg * s.dkp * s.dvp * 4, chans = (size_t)s.heads * s.nseg * s.dkp * 4;
   if (s.nseg > 1) {
     s.slots = take(states);
-    s.sums = take(chans);
+    s.decays = take(chans);
     if (backward) {
       s.slots2 = take(states);
-      s.sums2 = take(chans);
+      s.decays2 = take(chans);
     }
   }
   if (backward) {
@@ -291,9 +291,9 @@ hipError_t launch(ScanFn fn, int64_t grid, int waves, size_t lds, const mbd::Sca
   return hipLaunchKernel((const void*)fn, dim3((unsigned)grid), dim3((unsigned)waves * 64u), args, lds, stream);
 }
 
-hipError_t launch_join(const gla_scan_t* p, const ScanPlan& s, float* slots, const float* sums, const float* S0,
+hipError_t launch_join(const gla_scan_t* p, const ScanPlan& s, float* slots, const float* decays, const float* S0,
                        int rev, hipStream_t stream) {
-  mbd::JoinArgs j = {slots, sums, S0, p->offsets, p->rows, p->tokens, (int32_t)p->heads, (int32_t)p->dk,
+  mbd::JoinArgs j = {slots, decays, S0, p->offsets, p->rows, p->tokens, (int32_t)p->heads, (int32_t)p->dk,
                      (int32_t)p->dv, s.dkp, s.dvp, s.nseg, s.L, rev};
   void* args[] = {(void*)&j};
   const int64_t nx = ((int64_t)s.dkp * (s.dvp / 4) + 255) / 256;
@@ -381,7 +381,7 @@ extern "C" gemv_status_t gla_scan_forward(gemv_handle_t h, const gla_scan_t* p, 
   if (s.nseg > 1) {
     char* w = (char*)workspace;
     a.slots = (float*)(w + s.slots);
-    a.sums = (float*)(w + s.sums);
+    a.decays = (float*)(w + s.decays);
     // a segment's own state: columns in blocks of at most 256, channels in blocks of a workgroup's
     mbd::ScanArgs b = a;
     const int kw = waves_of(p->dk);
@@ -393,7 +393,7 @@ extern "C" gemv_status_t gla_scan_forward(gemv_handle_t h, const gla_scan_t* p, 
       b.ecol = (int32_t)c0;
       e = launch(scan_form(kScanState, p, 0, tier(c), kw == 4), bh * s.nseg * b.nblk, kw, kGradLds[tier(c)], b, stream);
     }
-    if (e == hipSuccess) e = launch_join(p, s, a.slots, a.sums, S0, 0, stream);
+    if (e == hipSuccess) e = launch_join(p, s, a.slots, a.decays, S0, 0, stream);
   }
   const int ow = waves_of(a.cols);
   if (e == hipSuccess) e = launch(scan_form(kScanOut, p, 0, tier(p->dk), ow == 4), grid, ow, kOutLds[tier(p->dk)], a, stream);
@@ -455,14 +455,14 @@ extern "C" gemv_status_t gla_scan_backward(gemv_handle_t h, const gla_scan_t* p,
   hipError_t e = hipSuccess;
   if (s.nseg > 1) {
     f.slots = (float*)(w + s.slots);
-    f.sums = (float*)(w + s.sums);
+    f.decays = (float*)(w + s.decays);
     r.slots = o.slots = (float*)(w + s.slots2);
-    r.sums = o.sums = (float*)(w + s.sums2);
+    r.decays = o.decays = (float*)(w + s.decays2);
     f.others = r.slots;
     e = launch(scan_form(kScanState, p, 0, vt, kw == 4), gk_grid, kw, kGradLds[vt], f, stream);
     if (e == hipSuccess) e = launch(scan_form(kScanState, p, 1, vt, kw == 4), gk_grid, kw, kGradLds[vt], r, stream);
-    if (e == hipSuccess) e = launch_join(p, s, f.slots, f.sums, S0, 0, stream);
-    if (e == hipSuccess) e = launch_join(p, s, r.slots, r.sums, dST, 1, stream);
+    if (e == hipSuccess) e = launch_join(p, s, f.slots, f.decays, S0, 0, stream);
+    if (e == hipSuccess) e = launch_join(p, s, r.slots, r.decays, dST, 1, stream);
   }
   if (e == hipSuccess) e = launch(scan_form(kScanGrad, p, 0, vt, kw == 4), gk_grid, kw, kGradLds[vt], f, stream);
   if (e == hipSuccess) e = launch(scan_form(kScanGrad, p, 1, vt, kw == 4), gk_grid, kw, kGradLds[vt], r, stream);

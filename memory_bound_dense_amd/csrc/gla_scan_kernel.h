@@ -78,7 +78,7 @@ struct ScanArgs {
   const float* S0;         // state before the first chunk (user layout), or null: zeros
   float* ST;               // state after the last chunk (user layout), or null
   float* slots;            // per segment: its start state, [dkp][dvp]; null: one segment
-  float* sums;             // state-only: sum of the gates of a segment, [dkp]
+  float* decays;           // state-only: a segment's whole decay, [dkp]
   const float* others;     // grad, forward: the slots of the reversed recurrence, or null
   const float* dST;        // grad, forward: dS_T or null
   float* ends;             // grad: rowsum(S D) at the end of each segment, [dkp]
@@ -208,11 +208,17 @@ __device__ __forceinline__ Lane lane_of(const ScanTensor& x, int g, int c0, int 
   l.step = (uint32_t)x.st * bytes;
   return l;
 }
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t chunk_rsrc(const ScanTensor& x, const char* base, int64_t tok,
-                                                             int n, int width, int bytes) {
-  // n valid tokens from tok on (none: an empty range)
+// The n valid tokens at `at` (none: an empty range).
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t chunk_rsrc(const ScanTensor& x, const char* at, int n, int width,
+                                                             int bytes) {
   const uint32_t len = n > 0 ? ((uint32_t)(n - 1) * (uint32_t)x.st + (uint32_t)width) * bytes : 0u;
-  return make_rsrc(base + tok * (int64_t)x.st * bytes, len);
+  return make_rsrc(at, len);
+}
+// To the next chunk in the order of the recurrence.
+template <bool REV>
+__device__ __forceinline__ void walk(const ScanTensor& x, const char*& at, int bytes) {
+  const int64_t by = (int64_t)(kScanC * bytes) * x.st;
+  at += REV ? -by : by;
 }
 // The lane's offsets as the loop's own values: the 8 tokens' offsets are then
 // formed where they are used, not kept in 8 registers per tensor over the loop.
@@ -279,57 +285,43 @@ struct Gates {
   float up[2][8];     // e^{G - r}
   float down[2][8];   // e^{r - G}
   float a[2], b[2];   // e^{r}, e^{end - r}: the whole chunk's decay, in two halves
-  float sum[2];       // end
   bool hard;
 };
-// Gates are summed as whole multiples of 2^-25 in units of log 2: exact sums
-// (modulo 2^32, which leaves differences within the range right), each gate
-// within 2^-25, and an exponential is 2^fraction scaled by the whole part.
-// Summed in fp32, chunks of strong gates lose up to 2^-24 |G| (1e-6 at |G| =
-// 20) in every decay, and a correctly rounded e^x costs more instructions.
-constexpr float kFix = 33554432.0f * 1.44269504f;
-static_assert(kRange * 1.4427f < 63.0f, "G - r as a multiple of 2^-25 has to fit 32 bits");
-// 2^(d / 2^25 + 1) / 2 in two factors: 2^(1 + fraction) in [2, 4) and a power of two.
-__device__ __forceinline__ float fraction_exp(int32_t d) {
-  return __builtin_amdgcn_exp2f(__builtin_bit_cast(float, (((uint32_t)d >> 2) & 0x7fffffu) | 0x3f800000u));
-}
-__device__ __forceinline__ float exp_fix(int32_t d) { return __builtin_amdgcn_ldexpf(fraction_exp(d), (d >> 25) - 1); }
+// Decays are products of the gates' exponentials, from the middle of the chunk
+// outwards: each factor is within about 2^-24, so a decay over i tokens within
+// about sqrt(i) 2^-24, whatever its size (a sum of gates in fp32, |G| = 20,
+// loses 1e-6), and an element costs one exponential, one reciprocal and three
+// products.
 template <int DT, bool G32, bool REV>
 __device__ __forceinline__ void make_gates(const uint32_t (&w)[kGateWords<G32>], int lane, Gates& q) {
   const int g = lane >> 4;
   float total = 0.0f;
 #pragma unroll
   for (int c = 0; c < 2; ++c) {
-    int32_t run = 0, G[8];
-    float size = 0.0f;
+    float run = 1.0f, size = 0.0f, P[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const float x = gate_value<DT, G32>(w, c, j);
       size += __builtin_fabsf(x);
-      if (REV) G[j] = run;
-      run += (int32_t)(x * kFix);
-      if (!REV) G[j] = run;
+      const float e = __builtin_amdgcn_exp2f(x * 1.44269504f);
+      if (REV) P[j] = run;
+      run = j == 0 ? e : run * e;
+      if (!REV) P[j] = run;
+    }
+    // the lane groups' products: 0 and 1 before the middle, 2 and 3 behind it
+    const float next = __shfl_xor(run, 16, 64), both = run * next;
+    const float other = __shfl_xor(both, 32, 64);
+    q.a[c] = g < 2 ? both : other;
+    q.b[c] = g < 2 ? other : both;
+    const float inv = __builtin_amdgcn_rcpf(g == 0 ? both : run);
+    const float f = g == 2 ? 1.0f : g == 3 ? next : inv;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      q.up[c][j] = P[j] * f;
+      q.down[c][j] = __builtin_amdgcn_rcpf(q.up[c][j]);
     }
     total = __builtin_fmaxf(total, size);
     if (!(size <= kRange)) total = __builtin_inff();   // NaN too
-    int32_t a = run;
-    const int32_t u = __shfl_up(a, 16, 64);
-    if (g >= 1) a += u;
-    const int32_t v = __shfl_up(a, 32, 64);
-    if (g >= 2) a += v;
-    const int32_t mid = __shfl(a, 16 + (lane & 15), 64);
-    const int32_t end = __shfl(a, 48 + (lane & 15), 64);
-    const int32_t base = a - run - mid;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int32_t d = base + G[j], whole = d >> 25;
-      const float p = fraction_exp(d);
-      q.up[c][j] = __builtin_amdgcn_ldexpf(p, whole - 1);
-      q.down[c][j] = __builtin_amdgcn_ldexpf(__builtin_amdgcn_rcpf(p), 1 - whole);
-    }
-    q.a[c] = exp_fix(mid);
-    q.b[c] = exp_fix(end - mid);
-    q.sum[c] = ((float)mid + (float)(end - mid)) * (1.0f / kFix);
   }
   // |G - r| <= the sum of |g| over one half of the chunk (two lane groups)
   total += __shfl_xor(total, 16, 64);
@@ -347,9 +339,6 @@ template <int DT>
 __device__ __forceinline__ bool pair_wild(uint32_t m) {
   constexpr uint32_t e = DT == DT_F16 ? 0x7c00u : 0x7f80u;
   return (m & 0xffffu) >= e || (m >> 16) >= e;
-}
-__device__ __forceinline__ float max3(float m, float a, float b) {
-  return __builtin_fmaxf(__builtin_fmaxf(m, __builtin_fabsf(a)), __builtin_fabsf(b));
 }
 
 // Two channels' columns (token-major pairs) as channel-major operands.
@@ -403,8 +392,11 @@ __device__ __forceinline__ bool place_of(const ScanArgs& a, Place& p) {
   p.last = p.len <= p.lo + a.L;
   return p.seg == 0 || p.lo < p.len;
 }
+// The first chunk of the segment in the order of the recurrence.
+template <bool REV>
 __device__ __forceinline__ const char* base_of(const ScanTensor& x, const Place& p, int bytes) {
-  return (const char*)x.p + (p.b * x.sb + p.h * x.sh + p.row0 * (int64_t)x.st) * bytes;
+  const int64_t tok = p.lo + (REV && p.hi > p.lo ? (p.hi - p.lo - 1) / kScanC * kScanC : 0);
+  return (const char*)x.p + (p.b * x.sb + p.h * x.sh + (p.row0 + tok) * (int64_t)x.st) * bytes;
 }
 // Row `m` of tile `tile` of a result: the token or channel 8 (m / 4) + 4 tile + m % 4.
 __device__ __forceinline__ int row_of(int m, int tile) { return 8 * (m >> 2) + 4 * tile + (m & 3); }
@@ -452,7 +444,6 @@ __device__ __forceinline__ void step_gates(const Step& t, const uint32_t (&gw)[k
         x = (t.pos & 7) == j ? gate_value<DT, G32>(gw, c, j) : x;
       }
       x = __shfl(x, 2 * (t.pos & ~7) + (lane & 15), 64);
-      q.sum[c] = x;
       q.a[c] = REV ? 1.0f : expf(x);
       q.b[c] = REV ? expf(x) : 1.0f;
     }
@@ -529,8 +520,8 @@ __global__ __launch_bounds__(NW * 64, NS > 4 ? 1 : 2) void scan_out_kernel(const
         }
   }
 
-  const char *kb = base_of(a.K, p, 2), *vb = base_of(a.V, p, 2), *xb = base_of(a.X, p, 2),
-             *gbp = base_of(a.G, p, gb), *ob = base_of(a.O, p, 2);
+  const char *kb = base_of<REV>(a.K, p, 2), *vb = base_of<REV>(a.V, p, 2), *xb = base_of<REV>(a.X, p, 2),
+             *gbp = base_of<REV>(a.G, p, gb), *ob = base_of<REV>(a.O, p, 2);
   const Lane vl = lane_of<REV>(a.V, g, col, vwidth, 2), ol = lane_of<REV>(a.O, g, col, vwidth, 2);
   Lane xl[SL], kl[SL], gl[SL];
 #pragma unroll
@@ -545,15 +536,19 @@ __global__ __launch_bounds__(NW * 64, NS > 4 ? 1 : 2) void scan_out_kernel(const
   auto fetch = [&](int c) {
     const int64_t tok = p.lo + (int64_t)(REV ? nch - 1 - c : c) * kScanC;
     const int nv = (int)min((int64_t)kScanC, p.hi - tok);
-    const auto gr = chunk_rsrc(a.G, gbp, tok, nv, a.dk, gb), kr = chunk_rsrc(a.K, kb, tok, nv, a.dk, 2),
-               xr = chunk_rsrc(a.X, xb, tok, nv, a.dk, 2);
+    const auto gr = chunk_rsrc(a.G, gbp, nv, a.dk, gb), kr = chunk_rsrc(a.K, kb, nv, a.dk, 2),
+               xr = chunk_rsrc(a.X, xb, nv, a.dk, 2);
 #pragma unroll
     for (int i = 0; i < SL; ++i) {
       load_gates<REV, G32>(gr, gl[i], a.G.vec, gw[i]);
       load16<REV>(kr, kl[i], a.K.vec, kw[i]);
       load16<REV>(xr, xl[i], a.X.vec, xw[i]);
     }
-    load16<REV>(chunk_rsrc(a.V, vb, tok, nv, a.dv, 2), vl, a.V.vec, vw);
+    load16<REV>(chunk_rsrc(a.V, vb, nv, a.dv, 2), vl, a.V.vec, vw);
+    walk<REV>(a.G, gbp, gb);
+    walk<REV>(a.K, kb, 2);
+    walk<REV>(a.X, xb, 2);
+    walk<REV>(a.V, vb, 2);
   };
   if (nch > 0) fetch(0);
   // a step's second half e^{end-r} is left to the next step, which scales the
@@ -572,21 +567,20 @@ __global__ __launch_bounds__(NW * 64, NS > 4 ? 1 : 2) void scan_out_kernel(const
       if (NS % NW != 0 && s >= NS) break;
       Gates q;
       step_gates<DT, G32, REV>(st, gw[i], lane, q);
-      uint32_t xt[8], kv[8], raw = 0, kt3[3][8];
+      uint32_t xt[8], kv[8], kt3[3][8];
       take(st, g, xw[i], xt);
       take(st, g, kw[i], kv);
       float big = 0.0f;
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const int row = 8 * g + j;
-        raw = pair_max(pair_max(raw, xt[j]), kv[j]);
         const float x0 = pair_lo<DT>(xt[j]) * q.up[0][j], x1 = pair_hi<DT>(xt[j]) * q.up[1][j];
         float k0 = pair_lo<DT>(kv[j]) * q.down[0][j], k1 = pair_hi<DT>(kv[j]) * q.down[1][j];
         if (REV) {
           k0 *= a.kscale;
           k1 *= a.kscale;
         }
-        big = max3(max3(big, x0, x1), k0, k1);
+        big += (__builtin_fabsf(x0) + __builtin_fabsf(x1)) + (__builtin_fabsf(k0) + __builtin_fabsf(k1));
         uint32_t t[2], u[3];
         split2<2>(x0, x1, t);
         *(uint32_t*)(xs + row * RS + d0) = t[0];
@@ -610,7 +604,7 @@ __global__ __launch_bounds__(NW * 64, NS > 4 ? 1 : 2) void scan_out_kernel(const
       }
       half[i][0] = q.b[0];
       half[i][1] = q.b[1];
-      hard |= q.hard || !(big <= kBig) || pair_wild<DT>(raw);
+      hard |= q.hard || !(big <= kBig);   // NaN too
     }
     uint32_t vv[8], rawv = 0;
     take(st, g, vw, vv);
@@ -702,13 +696,14 @@ __global__ __launch_bounds__(NW * 64, NS > 4 ? 1 : 2) void scan_out_kernel(const
 #pragma unroll
         for (int nt = 0; nt < 2; ++nt) S[s][tl][nt] = mfma_terms(kk, vt[nt], S[s][tl][nt]);
       }
-    const __amdgpu_buffer_rsrc_t orsrc = chunk_rsrc(a.O, ob, tok, nv, a.dv, 2);
+    const __amdgpu_buffer_rsrc_t orsrc = chunk_rsrc(a.O, ob, nv, a.dv, 2);
     const Lane ot = fresh(ol);
 #pragma unroll
     for (int j = 0; j < 8; ++j)
       if (now.width == 32 || takes(now, g, j))
         store16<REV>(orsrc, ot, a.O.vec, j,
                      pair_round<DT>(o[j >> 2][0][j & 3] * a.oscale, o[j >> 2][1][j & 3] * a.oscale));
+    if (next != c) walk<REV>(a.O, ob, 2);
     c = next;
     __syncthreads();
   }
@@ -791,15 +786,15 @@ __global__ __launch_bounds__(NW * 64, NV > 4 ? 1 : 2) void scan_grad_kernel(cons
         S[s][tl][nt] = x;
       }
 
-  const char *kb = base_of(a.K, p, 2), *vb = base_of(a.V, p, 2), *gbp = base_of(a.G, p, gb);
+  const char *kb = base_of<REV>(a.K, p, 2), *vb = base_of<REV>(a.V, p, 2), *gbp = base_of<REV>(a.G, p, gb);
   const char *xb = nullptr, *wb = nullptr, *ob = nullptr, *dgb = nullptr;
   float* qdq = nullptr;
-  float carry[2] = {0.0f, 0.0f}, gsum[2] = {0.0f, 0.0f};
+  float carry[2] = {0.0f, 0.0f}, all_decay[2] = {1.0f, 1.0f};
   if (GRAD) {
-    xb = base_of(a.X, p, 2);
-    wb = base_of(a.W, p, 2);
-    ob = base_of(a.O, p, 2);
-    if (REV) dgb = base_of(a.DG, p, gb);
+    xb = base_of<REV>(a.X, p, 2);
+    wb = base_of<REV>(a.W, p, 2);
+    ob = base_of<REV>(a.O, p, 2);
+    if (REV) dgb = base_of<REV>(a.DG, p, gb);
     // rows of all sequences in one run: (b t + token, h, dkp)
     qdq = a.qdq + ((p.b * a.t + p.row0) * a.H + p.h) * a.dkp;
     if (REV) {
@@ -827,16 +822,20 @@ __global__ __launch_bounds__(NW * 64, NV > 4 ? 1 : 2) void scan_grad_kernel(cons
   auto fetch = [&](int c) {
     const int64_t tok = p.lo + (int64_t)(REV ? nch - 1 - c : c) * kScanC;
     const int nv = (int)min((int64_t)kScanC, p.hi - tok);
-    const auto vr = chunk_rsrc(a.V, vb, tok, nv, a.dv, 2);
+    const auto vr = chunk_rsrc(a.V, vb, nv, a.dv, 2);
 #pragma unroll
     for (int i = 0; i < SL; ++i) load16<REV>(vr, vl[i], a.V.vec, vw[i]);
     if (GRAD) {
-      const auto wr = chunk_rsrc(a.W, wb, tok, nv, a.dv, 2);
+      const auto wr = chunk_rsrc(a.W, wb, nv, a.dv, 2);
 #pragma unroll
       for (int i = 0; i < SL; ++i) load16<REV>(wr, wl[i], a.W.vec, ww[i]);
+      walk<REV>(a.W, wb, 2);
     }
-    load_gates<REV, G32>(chunk_rsrc(a.G, gbp, tok, nv, a.dk, gb), gl, a.G.vec, gw);
-    load16<REV>(chunk_rsrc(a.K, kb, tok, nv, a.dk, 2), kl, a.K.vec, kw);
+    load_gates<REV, G32>(chunk_rsrc(a.G, gbp, nv, a.dk, gb), gl, a.G.vec, gw);
+    load16<REV>(chunk_rsrc(a.K, kb, nv, a.dk, 2), kl, a.K.vec, kw);
+    walk<REV>(a.V, vb, 2);
+    walk<REV>(a.G, gbp, gb);
+    walk<REV>(a.K, kb, 2);
   };
   if (nch > 0) fetch(0);
   float left[2] = {1.0f, 1.0f};   // a step's second half e^{end-r}, done with the next step's first
@@ -874,22 +873,21 @@ __global__ __launch_bounds__(NW * 64, NV > 4 ? 1 : 2) void scan_grad_kernel(cons
     step_gates<DT, G32, REV>(st, gw, lane, q);
     bf16x8 kk[2][3];
     {
-      uint32_t kv[8], raw = 0;
+      uint32_t kv[8];
       float big = 0.0f;
       take(st, g, kw, kv);
       float kf[2][8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        raw = pair_max(raw, kv[j]);
         kf[0][j] = pair_lo<DT>(kv[j]) * q.down[0][j];
         kf[1][j] = pair_hi<DT>(kv[j]) * q.down[1][j];
         if (REV) {
           kf[0][j] *= a.kscale;
           kf[1][j] *= a.kscale;
         }
-        big = max3(big, kf[0][j], kf[1][j]);
+        big += __builtin_fabsf(kf[0][j]) + __builtin_fabsf(kf[1][j]);
       }
-      hard |= q.hard || !(big <= kBig) || pair_wild<DT>(raw);
+      hard |= q.hard || !(big <= kBig);   // NaN too
       split8<3>(kf[0], kk[0]);
       split8<3>(kf[1], kk[1]);
     }
@@ -905,15 +903,17 @@ __global__ __launch_bounds__(NW * 64, NV > 4 ? 1 : 2) void scan_grad_kernel(cons
       continue;
     }
 
-    gsum[0] += q.sum[0];
-    gsum[1] += q.sum[1];
+    if (!GRAD) {
+      all_decay[0] *= q.a[0] * q.b[0];
+      all_decay[1] *= q.a[1] * q.b[1];
+    }
 #pragma unroll
     for (int nt = 0; nt < 2; ++nt) {
       q.a[nt] *= left[nt];
       left[nt] = q.b[nt];
     }
     uint32_t xw[8];
-    if (GRAD) load16<REV>(chunk_rsrc(a.X, xb, tok, nv, a.dk, 2), xl, a.X.vec, xw);
+    if (GRAD) load16<REV>(chunk_rsrc(a.X, xb, nv, a.dk, 2), xl, a.X.vec, xw);
     const Step now = st;
     advance(st);
     const int next = st.pos == kScanC ? c + 1 : c;
@@ -978,7 +978,7 @@ __global__ __launch_bounds__(NW * 64, NV > 4 ? 1 : 2) void scan_grad_kernel(cons
           }
         }
       }
-      const __amdgpu_buffer_rsrc_t orsrc = chunk_rsrc(a.O, ob, tok, nv, a.dk, 2);
+      const __amdgpu_buffer_rsrc_t orsrc = chunk_rsrc(a.O, ob, nv, a.dk, 2);
       const Lane ot = fresh(ol);
       float y[2][8];
 #pragma unroll
@@ -1013,7 +1013,7 @@ __global__ __launch_bounds__(NW * 64, NV > 4 ? 1 : 2) void scan_grad_kernel(cons
             d[nt][j] = run[nt];
           }
         }
-        const __amdgpu_buffer_rsrc_t drsrc = chunk_rsrc(a.DG, dgb, tok, nv, a.dk, gb);
+        const __amdgpu_buffer_rsrc_t drsrc = chunk_rsrc(a.DG, dgb, nv, a.dk, gb);
         const Lane dt = fresh(dl);
 #pragma unroll
         for (int nt = 0; nt < 2; ++nt) {
@@ -1058,6 +1058,11 @@ __global__ __launch_bounds__(NW * 64, NV > 4 ? 1 : 2) void scan_grad_kernel(cons
 #pragma unroll
         for (int nt = 0; nt < 2; ++nt) S[s][tl][nt] = mfma_terms(vv, kk[nt], S[s][tl][nt]);
       }
+    if (GRAD && next != c) {
+      walk<REV>(a.X, xb, 2);
+      walk<REV>(a.O, ob, 2);
+      if (REV) walk<REV>(a.DG, dgb, gb);
+    }
     c = next;
     __syncthreads();
   }
@@ -1084,7 +1089,7 @@ __global__ __launch_bounds__(NW * 64, NV > 4 ? 1 : 2) void scan_grad_kernel(cons
     if (g == 0)
 #pragma unroll
       for (int nt = 0; nt < 2; ++nt)
-        if (col + nt < a.dkp) a.sums[p.slot * a.dkp + col + nt] = gsum[nt];
+        if (col + nt < a.dkp) a.decays[p.slot * a.dkp + col + nt] = all_decay[nt];
     return;
   }
   if (REV) {
