@@ -19,16 +19,22 @@ using GemmFn = void (*)(const mbd::GemmArgs);
 // Tiles: rows of B x tokens.
 struct Tile {
   int bn, bm, threads;
-  size_t lds;
+  size_t lds;        // dynamic
   GemmFn fn[3];
 };
 #define TILE(BN, BM, WN, WM)                                                                      \
   {BN, BM, WN * WM * 64, mbd::gemm_tile_lds<BN, BM>(),                                            \
    {&mbd::gemm_tile_kernel<0, BN, BM, WN, WM>, &mbd::gemm_tile_kernel<1, BN, BM, WN, WM>,         \
     &mbd::gemm_tile_kernel<2, BN, BM, WN, WM>}}
-const Tile kTiles[] = {TILE(256, 256, 2, 4), TILE(128, 256, 2, 2), TILE(128, 128, 2, 2), TILE(64, 128, 2, 2),
-                       TILE(64, 64, 2, 2)};
-constexpr int kNumTiles = sizeof(kTiles) / sizeof(kTiles[0]);
+#define DIRECT(BN, BM, WN, WM, WK, WN8, WM8)                                                            \
+  {BN, BM, WN * WM * WK * 64, 0,                                                                        \
+   {&mbd::gemm_direct_kernel<0, BN, BM, WN, WM, WK>, &mbd::gemm_direct_kernel<1, BN, BM, WN, WM, WK>,   \
+    &mbd::gemm_direct_kernel<2, BN, BM, WN8, WM8, 1>}}
+// largest first; [1]: rows on 16-byte boundaries
+const Tile kTiles[2][5] = {{TILE(256, 256, 2, 4), TILE(128, 256, 2, 2), TILE(128, 128, 2, 2), TILE(64, 128, 2, 2),
+                            TILE(64, 64, 2, 2)},
+                           {DIRECT(256, 256, 2, 4, 1, 2, 4), DIRECT(256, 128, 2, 2, 2, 4, 2),
+                            DIRECT(128, 128, 1, 2, 2, 2, 2), TILE(64, 128, 2, 2), TILE(64, 64, 2, 2)}};
 
 constexpr int kSkinnyWaves = 8;
 #define SKINNY(MT, U) \
@@ -36,18 +42,18 @@ constexpr int kSkinnyWaves = 8;
 const GemmFn kSkinny[2][3] = {SKINNY(1, 4), SKINNY(2, 2)};
 
 struct GemmPlan {
-  int tile;          // -1: skinny
+  const Tile* tile;  // null: skinny
   int mt;            // skinny: token tiles
   int64_t tiles_m, tiles_n, nsplit, npad;
   size_t bytes;
 };
 
-GemmPlan gemm_plan(const gemm_t* p) {
+// `whole`: rows of A and B on 16-byte boundaries.
+GemmPlan gemm_plan(const gemm_t* p, bool whole) {
   GemmPlan g = {};
   const int64_t slabs = (p->k * in_bytes(p->in_type) + 127) / 128;
   g.nsplit = 1;
   if (p->m <= 32) {
-    g.tile = -1;
     g.mt = p->m <= 16 ? 1 : 2;
     g.tiles_m = 1;
     g.tiles_n = (p->n + 15) / 16;
@@ -55,23 +61,24 @@ GemmPlan gemm_plan(const gemm_t* p) {
     g.nsplit = std::max(std::min(want, slabs / (kSkinnyWaves * 2)), (int64_t)1);
   } else {
     // the largest tile that still gives every CU one
-    g.tile = kNumTiles - 1;
-    for (int t = 0; t < kNumTiles; ++t) {
-      const int64_t c = ((p->m + kTiles[t].bm - 1) / kTiles[t].bm) * ((p->n + kTiles[t].bn - 1) / kTiles[t].bn);
-      if (c >= 256) {
-        g.tile = t;
-        break;
-      }
+    for (const Tile& t : kTiles[whole]) {
+      g.tile = &t;
+      if (((p->m + t.bm - 1) / t.bm) * ((p->n + t.bn - 1) / t.bn) >= 256) break;
     }
-    g.tiles_m = (p->m + kTiles[g.tile].bm - 1) / kTiles[g.tile].bm;
-    g.tiles_n = (p->n + kTiles[g.tile].bn - 1) / kTiles[g.tile].bn;
+    g.tiles_m = (p->m + g.tile->bm - 1) / g.tile->bm;
+    g.tiles_n = (p->n + g.tile->bn - 1) / g.tile->bn;
     const int64_t want = 256 / (g.tiles_m * g.tiles_n);
     g.nsplit = std::max(std::min(want, slabs / 8), (int64_t)1);
   }
   g.npad = up(p->n, 4);
-  if (g.tile < 0) g.npad = up(p->n, 16);
+  if (!g.tile) g.npad = up(p->n, 16);
   if (g.nsplit > 1) g.bytes = (size_t)g.nsplit * p->m * g.npad * 4;
   return g;
+}
+
+bool whole_rows(const gemm_t* p, const void* A, const void* B) {
+  const int64_t e = in_bytes(p->in_type);
+  return ((((uintptr_t)A | (uintptr_t)B) & 15u) | ((p->lda * e) & 15) | ((p->ldb * e) & 15)) == 0;
 }
 
 Region matrix(const void* x, int64_t rows, int64_t cols, int64_t ld, int64_t bytes) {
@@ -98,7 +105,7 @@ gemv_status_t check(const gemm_t* p, const void* A, const void* B, const void* C
   uintptr_t two = (uintptr_t)C | (uintptr_t)p->bias | (uintptr_t)p->residual;
   if (e == 2 && p->k > 0) two |= (uintptr_t)A | (uintptr_t)B;
   if ((two & 1u) || (((uintptr_t)p->scale_a | (uintptr_t)p->scale_b) & 3u)) return GEMV_ERR_MISALIGNED;
-  const GemmPlan g = gemm_plan(p);
+  const GemmPlan g = gemm_plan(p, whole_rows(p, A, B));
   if (g.bytes) {
     if (!workspace || workspace_bytes < g.bytes) return GEMV_ERR_INVALID_ARG;
     if ((uintptr_t)workspace & 15u) return GEMV_ERR_MISALIGNED;
@@ -122,16 +129,19 @@ gemv_status_t check(const gemm_t* p, const void* A, const void* B, const void* C
 }  // namespace
 
 bool mbd_host::gemm_set_attributes() {
-  for (const Tile& t : kTiles)
-    for (GemmFn f : t.fn)
-      if (hipFuncSetAttribute((const void*)f, hipFuncAttributeMaxDynamicSharedMemorySize, (int)t.lds) != hipSuccess)
-        return false;
+  for (const auto& set : kTiles)
+    for (const Tile& t : set)
+      for (GemmFn f : t.fn)
+        if (t.lds &&
+            hipFuncSetAttribute((const void*)f, hipFuncAttributeMaxDynamicSharedMemorySize, (int)t.lds) != hipSuccess)
+          return false;
   return true;
 }
 
 extern "C" size_t gemm_workspace_bytes(const gemm_t* p) {
   if (check(p, nullptr, nullptr, nullptr, nullptr, 0, true) != GEMV_OK || p->m == 0 || p->n == 0) return 0;
-  return gemm_plan(p).bytes;
+  // the pointers are not known here: what either kind of rows needs
+  return std::max(gemm_plan(p, false).bytes, gemm_plan(p, true).bytes);
 }
 
 extern "C" gemv_status_t gemm_check_args(const gemm_t* p, const void* A, const void* B, const void* C,
@@ -148,7 +158,7 @@ extern "C" gemv_status_t gemm_run(gemv_handle_t h, const gemm_t* p, const void* 
   int dev = -1;
   if (hipGetDevice(&dev) != hipSuccess) return report(h, GEMV_ERR_HIP, "hipGetDevice");
   if (dev != h->device) return report(h, GEMV_ERR_WRONG_DEVICE, "gemm_run");
-  const GemmPlan g = gemm_plan(p);
+  const GemmPlan g = gemm_plan(p, whole_rows(p, A, B));
   const int64_t e = in_bytes(p->in_type);
   mbd::GemmArgs a = {};
   a.A = (const uint8_t*)A;
@@ -176,15 +186,15 @@ extern "C" gemv_status_t gemm_run(gemv_handle_t h, const gemm_t* p, const void* 
   a.npad = (int32_t)g.npad;
   a.alpha = p->alpha;
   const int64_t grid = g.tiles_m * g.tiles_n * g.nsplit;
-  const int threads = g.tile < 0 ? kSkinnyWaves * 64 : kTiles[g.tile].threads;
+  const int threads = g.tile ? g.tile->threads : kSkinnyWaves * 64;
   const int64_t jgrid = g.nsplit > 1 ? (p->m * (g.npad / 4) + 255) / 256 : 0;
   // a grid's work-items along x (a 32-bit field of the dispatch) are kept at most 2^31
   if (grid > ((int64_t)1 << 31) / threads || jgrid > ((int64_t)1 << 23))
     return report(h, GEMV_ERR_TOO_LARGE, "gemm_run grid");
   void* args[] = {(void*)&a};
-  const void* fn = (const void*)(g.tile < 0 ? kSkinny[g.mt - 1][p->in_type] : kTiles[g.tile].fn[p->in_type]);
+  const void* fn = (const void*)(g.tile ? g.tile->fn[p->in_type] : kSkinny[g.mt - 1][p->in_type]);
   hipError_t err = hipLaunchKernel(fn, dim3((unsigned)grid), dim3((unsigned)threads), args,
-                                   g.tile < 0 ? 0 : kTiles[g.tile].lds, stream);
+                                   g.tile ? g.tile->lds : 0, stream);
   if (err == hipSuccess && g.nsplit > 1)
     err = hipLaunchKernel((const void*)&mbd::gemm_join_kernel, dim3((unsigned)jgrid), dim3(256), args, 0, stream);
   return err == hipSuccess ? GEMV_OK : report(h, GEMV_ERR_HIP, hipGetErrorString(err));

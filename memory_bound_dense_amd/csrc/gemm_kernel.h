@@ -79,6 +79,16 @@ __device__ __forceinline__ f32x4 slab_mfma(const u32x4 (&a)[2], const u32x4 (&b)
   }
 }
 
+// c += a b over half a slab (16-bit types).
+template <int IN>
+__device__ __forceinline__ f32x4 half_mfma(u32x4 a, u32x4 b, f32x4 c) {
+  if constexpr (IN == IN_F16)
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0,
+                                                   0);
+}
+
 // 16 bytes at `off` of a row of which `left` bytes are valid from there on
 // (the rest reads as 0): element by element where fewer than 16 are left, so
 // nothing behind the row is read.
@@ -99,52 +109,127 @@ __device__ __forceinline__ u32x4 load_chunk(__amdgpu_buffer_rsrc_t r, uint32_t o
   return u32x4{w[0], w[1], w[2], w[3]};
 }
 
-__device__ __forceinline__ float activate(float y, int act) {
-  switch (act) {
-    case ACT_RELU: return y < 0.0f ? 0.0f : y;
-    case ACT_GELU: return 0.5f * y * erfcf(-0.707106781f * y);
-    case ACT_GELU_TANH: return 0.5f * y * (1.0f + tanhf(0.797884561f * __builtin_fmaf(0.044715f * y * y, y, y)));
-    case ACT_SILU: return y / (1.0f + expf(-y));
-    default: return y;
+// The hardware's 2^x and reciprocal (each within one unit in the last place)
+// stand in for e^x and division: silu and tanh are within a few units.
+template <int ACT>
+__device__ __forceinline__ float activate(float y) {
+  if constexpr (ACT == ACT_RELU) return y < 0.0f ? 0.0f : y;
+  else if constexpr (ACT == ACT_GELU) return 0.5f * y * erfcf(-0.707106781f * y);
+  else if constexpr (ACT == ACT_GELU_TANH) {
+    // (1 + tanh u) / 2 = 1 / (1 + e^-2u)
+    const float u = 0.797884561f * __builtin_fmaf(0.044715f * y * y, y, y);
+    return y * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(u * -2.88539008f));
+  } else if constexpr (ACT == ACT_SILU) return y * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(y * -1.44269504f));
+  else return y;
+}
+template <int ACT>
+__device__ __forceinline__ void activate4(float (&y)[4]) {
+#pragma unroll
+  for (int x = 0; x < 4; ++x) y[x] = activate<ACT>(y[x]);
+}
+__device__ __forceinline__ void widen4(u32x2 w, int out, float (&x)[4]) {
+  const uint32_t a = w[0], b = w[1];
+  const uint16_t h[4] = {(uint16_t)a, (uint16_t)(a >> 16), (uint16_t)b, (uint16_t)(b >> 16)};
+  if (out == DT_F16) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = widen<DT_F16>(h[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = widen<DT_BF16>(h[i]);
   }
 }
-__device__ __forceinline__ float widen_out(uint16_t x, int out) {
-  return out == DT_F16 ? widen<DT_F16>(x) : widen<DT_BF16>(x);
+__device__ __forceinline__ u32x2 round4(const float (&x)[4], int out) {
+  uint16_t h[4];
+  if (out == DT_F16) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) h[i] = to_bits<DT_F16>(x[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) h[i] = to_bits<DT_BF16>(x[i]);
+  }
+  return u32x2{(uint32_t)h[0] | (uint32_t)h[1] << 16, (uint32_t)h[2] | (uint32_t)h[3] << 16};
 }
-__device__ __forceinline__ uint16_t round_out(float x, int out) {
-  return out == DT_F16 ? to_bits<DT_F16>(x) : to_bits<DT_BF16>(x);
+// 4 consecutive 16-bit values of which `left` exist (the others read as 0).
+__device__ __forceinline__ u32x2 load4(const uint16_t* p, bool whole, int left) {
+  if (whole && left >= 4) return *(const u32x2*)p;
+  uint32_t h[4];
+#pragma unroll
+  for (int x = 0; x < 4; ++x) h[x] = x < left ? p[x] : 0u;
+  return u32x2{h[0] | h[1] << 16, h[2] | h[3] << 16};
 }
 
-// The epilogue of 4 consecutive outputs j.. of token i, and their store.
-__device__ __forceinline__ void finish4(const GemmArgs& p, int64_t i, int j, f32x4 s) {
-  if (i >= p.m || j >= p.n) return;
-  const float f = p.sa ? p.alpha * p.sa[i] : p.alpha;
-  const int64_t at = i * p.ldc + j, rt = i * p.ldr + j;
-  if (p.vec && j + 4 <= p.n) {
-    uint16_t r[4] = {}, o[4];
-    if (p.res) *(u32x2*)r = *(const u32x2*)(p.res + rt);
-#pragma unroll
-    for (int x = 0; x < 4; ++x) {
-      float y = s[x] * f;
-      if (p.sb) y *= p.sb[j + x];
-      if (p.bias) y += widen_out(p.bias[j + x], p.out);
-      y = activate(y, p.act);
-      if (p.res) y += widen_out(r[x], p.out);
-      o[x] = round_out(y, p.out);
-    }
-    *(u32x2*)(p.C + at) = *(const u32x2*)o;
-    return;
-  }
+// What the epilogue of 4 consecutive outputs j.. takes from their columns.
+struct Columns {
+  float scale[4], bias[4];
+};
+__device__ __forceinline__ Columns columns_at(const GemmArgs& p, int j) {
+  Columns c;
 #pragma unroll
   for (int x = 0; x < 4; ++x) {
-    if (j + x < p.n) {
-      float y = s[x] * f;
-      if (p.sb) y *= p.sb[j + x];
-      if (p.bias) y += widen_out(p.bias[j + x], p.out);
-      y = activate(y, p.act);
-      if (p.res) y += widen_out(p.res[rt + x], p.out);
-      p.C[at + x] = round_out(y, p.out);
+    const bool in = j + x < p.n;
+    c.scale[x] = p.sb && in ? p.sb[j + x] : 1.0f;
+    c.bias[x] = 0.0f;
+  }
+  if (p.bias && j < p.n) widen4(load4(p.bias + j, false, p.n - j), p.out, c.bias);
+  return c;
+}
+// The epilogue of outputs j .. j+3 of token i from their sums, and their store.
+__device__ __forceinline__ void finish4(const GemmArgs& p, int64_t i, int j, f32x4 s, const Columns& c) {
+  if (i >= p.m || j >= p.n) return;
+  const float f = p.sa ? p.alpha * p.sa[i] : p.alpha;
+  float y[4], r[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  if (p.res) widen4(load4(p.res + i * p.ldr + j, p.vec, p.n - j), p.out, r);
+#pragma unroll
+  for (int x = 0; x < 4; ++x) y[x] = s[x] * f * c.scale[x] + c.bias[x];
+  switch (p.act) {
+    case ACT_RELU: activate4<ACT_RELU>(y); break;
+    case ACT_GELU: activate4<ACT_GELU>(y); break;
+    case ACT_GELU_TANH: activate4<ACT_GELU_TANH>(y); break;
+    case ACT_SILU: activate4<ACT_SILU>(y); break;
+    default: break;
+  }
+#pragma unroll
+  for (int x = 0; x < 4; ++x) y[x] += r[x];
+  const u32x2 o = round4(y, p.out);
+  uint16_t* to = p.C + i * p.ldc + j;
+  if (p.vec && j + 4 <= p.n) {
+    *(u32x2*)to = o;
+  } else {
+#pragma unroll
+    for (int x = 0; x < 4; ++x)
+      if (j + x < p.n) to[x] = (uint16_t)(o[x >> 1] >> (16 * (x & 1)));
+  }
+}
+
+// A wave's accumulators out through LDS, 16 tokens at a time: its lanes then
+// hold consecutive outputs of a token, and the epilogue's code is there once.
+// `mine`: the wave's own 16 x (16 TN + 4) floats.
+template <int TN, int TM>
+__device__ __forceinline__ void write_tile(const GemmArgs& p, const f32x4 (&c)[TN][TM], float* mine, int lane,
+                                           int row0, int col0, int sp) {
+  constexpr int RS = TN * 16 + 4, LPR = TN * 4;   // floats per staged row; lanes per row
+  const int r = lane & 15, g = lane >> 4;
+  static_assert(LPR <= 64 && 64 % LPR == 0, "a lane keeps its columns");
+  const int at = (lane % LPR) * 4, j = col0 + at;
+  const Columns cols = columns_at(p, j);
+#pragma unroll 1
+  for (int t = 0; t < TM; ++t) {
+#pragma unroll
+    for (int tt = 0; tt < TM; ++tt)
+      if (t == tt) {
+#pragma unroll
+        for (int n = 0; n < TN; ++n) *(f32x4*)(mine + r * RS + 16 * n + 4 * g) = c[n][tt];
+      }
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+#pragma unroll 1
+    for (int row = lane / LPR; row < 16; row += 64 / LPR) {
+      const f32x4 v = *(const f32x4*)(mine + row * RS + at);
+      const int i = row0 + t * 16 + row;
+      if (p.nsplit == 1) finish4(p, i, j, v, cols);
+      else if (i < p.m && j < p.npad) *(f32x4*)(p.part + ((int64_t)sp * p.m + i) * p.npad + j) = v;
     }
+    __builtin_amdgcn_wave_barrier();
   }
 }
 
@@ -215,7 +300,7 @@ __global__ __launch_bounds__(W * 64) void gemm_skinny_kernel(const GemmArgs p) {
 #pragma unroll
     for (int w = 0; w < W; ++w) v += *(const f32x4*)&sums[w][t][l * 4];
     const int i = 16 * t + (l & 15), j = row0 + 4 * (l >> 4);
-    if (p.nsplit == 1) finish4(p, i, j, v);
+    if (p.nsplit == 1) finish4(p, i, j, v, columns_at(p, j));
     else if (i < p.m) *(f32x4*)(p.part + ((int64_t)sp * p.m + i) * p.npad + j) = v;
   }
 }
@@ -328,30 +413,157 @@ __global__ __launch_bounds__(WN * WM * 64, (WN * WM > 4 ? 2 : 1)) void gemm_tile
       __syncthreads();
     }
   }
-  // Out through LDS, 16 tokens at a time: a wave's lanes then hold consecutive
-  // outputs of a token, and the epilogue's code is there once.
-  constexpr int RS = TN * 16 + 4, LPR = TN * 4;   // floats per staged row; lanes per row
-  float* mine = (float*)smem + wave * 16 * RS;
-#pragma unroll 1
-  for (int t = 0; t < TM; ++t) {
+  constexpr int RS = TN * 16 + 4;
+  write_tile<TN, TM>(p, c, (float*)smem + wave * 16 * RS, lane, tm0 + wm * TM * 16, tn0 + wn * TN * 16, sp);
+}
+
+__device__ __forceinline__ void load_to_lds(__amdgpu_buffer_rsrc_t r, uint8_t* to, uint32_t off) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)to, 16, off, 0, 0, 0);
+}
+
+// ---- many tokens, rows on 16-byte boundaries ----------------------------------
+// The same tile with loads that write LDS directly (no registers, no LDS store
+// instructions), so a slab is on its way into one buffer while the other is
+// used; the two buffers are separate objects, which lets the compiler see that
+// reading one does not wait for loads into the other.  LDS takes lane l's 16
+// bytes at 16 l of a wave's 1 KiB (8 rows), so the chunk swizzle is applied to
+// the address a lane fetches.  WK = 2: two waves share each wave tile, each
+// with one 64-byte half of every slab, and add their sums at the end -- the
+// operand traffic of 4 big wave tiles with 8 waves to hide its latency.
+
+template <int IN, int BN, int BM, int WN, int WM, int WK>
+__global__ __launch_bounds__(WN * WM * WK * 64, 2) void gemm_direct_kernel(const GemmArgs p) {
+  constexpr int W = WN * WM * WK, R8 = (BN + BM) / 8, LPW = R8 / W;   // 1 KiB loads per wave and slab
+  constexpr int TN = BN / WN / 16, TM = BM / WM / 16;
+  constexpr int RS = TN * 16 + 4;
+  static_assert(R8 % W == 0 && BN % 8 == 0, "");
+  static_assert(WK == 1 || IN != IN_E4M3, "an 8-bit instruction takes a whole slab");
+  __shared__ __attribute__((aligned(16))) uint8_t buf0[(BN + BM) * 128];
+  __shared__ __attribute__((aligned(16))) uint8_t buf1[(BN + BM) * 128];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int r = lane & 15, g = lane >> 4;
+  const int wn = wave % WN, wm = (wave / WN) % WM, wk = wave / (WN * WM);
+
+  int64_t unit = xcd_unit(blockIdx.x, gridDim.x);
+  const int sp = (int)(unit % p.nsplit);
+  unit /= p.nsplit;
+  constexpr int GM = 8;
+  const int64_t per = (int64_t)GM * p.tiles_n;
+  const int grp = (int)(unit / per), in = (int)(unit % per);
+  const int gm = min(GM, p.tiles_m - grp * GM);
+  const int tm0 = (grp * GM + in % gm) * BM, tn0 = (in / gm) * BN;
+
+  const int rows_b = min(BN, p.n - tn0), rows_a = min(BM, p.m - tm0);
+  const __amdgpu_buffer_rsrc_t br =
+      make_rsrc(p.B + (int64_t)tn0 * p.ldb, (uint32_t)((int64_t)(rows_b - 1) * p.ldb + p.kbytes));
+  const __amdgpu_buffer_rsrc_t ar =
+      make_rsrc(p.A + (int64_t)tm0 * p.lda, (uint32_t)((int64_t)(rows_a - 1) * p.lda + p.kbytes));
+  // this wave's rows: 8 per load; rows of B first.  Rows behind the last one
+  // are left unfetched: they only reach outputs that are not stored.
+  const int chunk = ((lane & 7) ^ (lane >> 3)) * 16;
+  uint32_t off[LPW];
 #pragma unroll
-    for (int tt = 0; tt < TM; ++tt)
-      if (t == tt) {
-#pragma unroll
-        for (int n = 0; n < TN; ++n) *(f32x4*)(mine + r * RS + 16 * n + 4 * g) = c[n][tt];
-      }
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-#pragma unroll 1
-    for (int e = lane; e < 16 * LPR; e += 64) {
-      const int row = e / LPR, at = (e % LPR) * 4;
-      const f32x4 v = *(const f32x4*)(mine + row * RS + at);
-      const int i = tm0 + (wm * TM + t) * 16 + row, j = tn0 + wn * TN * 16 + at;
-      if (p.nsplit == 1) finish4(p, i, j, v);
-      else if (i < p.m && j < p.npad) *(f32x4*)(p.part + ((int64_t)sp * p.m + i) * p.npad + j) = v;
-    }
-    __builtin_amdgcn_wave_barrier();
+  for (int i = 0; i < LPW; ++i) {
+    const int row = (wave * LPW + i) * 8 + (lane >> 3);
+    if ((wave * LPW + i) * 8 < BN) off[i] = row < rows_b ? (uint32_t)(row * p.ldb) + chunk : kOffsetOutOfRange;
+    else off[i] = row - BN < rows_a ? (uint32_t)((row - BN) * p.lda) + chunk : kOffsetOutOfRange;
   }
+
+  const int full = p.kbytes >> 7, total = full + ((p.kbytes & 127) != 0);
+  const int q = total / p.nsplit, x = total % p.nsplit;
+  const int s0 = sp * q + min(sp, x), s1 = s0 + q + (sp < x);
+
+  auto issue = [&](uint8_t* buf, int s) {
+    const uint32_t o = (uint32_t)s * 128;
+    if (s < full) {
+#pragma unroll
+      for (int i = 0; i < LPW; ++i) {
+        const int r8 = wave * LPW + i;
+        load_to_lds(r8 * 8 < BN ? br : ar, buf + r8 * 1024, off[i] + o);
+      }
+    } else {
+      const int left = p.kbytes - (int)o - chunk;
+#pragma unroll
+      for (int i = 0; i < LPW; ++i) {
+        const int r8 = wave * LPW + i;
+        *(u32x4*)(buf + r8 * 1024 + lane * 16) = load_chunk<IN>(r8 * 8 < BN ? br : ar, off[i] + o, left);
+      }
+    }
+  };
+  f32x4 c[TN][TM] = {};
+  auto use = [&](const uint8_t* buf) {
+    const uint8_t* bb = buf + (wn * TN * 16 + r) * 128;
+    const uint8_t* ab = buf + (BN + wm * TM * 16 + r) * 128;
+    if constexpr (IN == IN_E4M3) {
+      const int c0 = (g ^ (r & 7)) * 16, c1 = ((4 + g) ^ (r & 7)) * 16;
+      u32x4 a[TM][2];
+#pragma unroll
+      for (int t = 0; t < TM; ++t) {
+        a[t][0] = *(const u32x4*)(ab + t * 16 * 128 + c0);
+        a[t][1] = *(const u32x4*)(ab + t * 16 * 128 + c1);
+      }
+#pragma unroll
+      for (int n = 0; n < TN; ++n) {
+        u32x4 b[2];
+        b[0] = *(const u32x4*)(bb + n * 16 * 128 + c0);
+        b[1] = *(const u32x4*)(bb + n * 16 * 128 + c1);
+#pragma unroll
+        for (int t = 0; t < TM; ++t) c[n][t] = slab_mfma<IN>(b, a[t], c[n][t]);
+      }
+    } else {
+#pragma unroll
+      for (int hh = 0; hh < 2 / WK; ++hh) {
+        const int h = WK == 2 ? wk : hh;
+        const int c0 = ((4 * h + g) ^ (r & 7)) * 16;
+        u32x4 a[TM];
+#pragma unroll
+        for (int t = 0; t < TM; ++t) a[t] = *(const u32x4*)(ab + t * 16 * 128 + c0);
+        u32x4 b = *(const u32x4*)(bb + c0);
+#pragma unroll
+        for (int n = 0; n < TN; ++n) {
+          u32x4 next = b;
+          if (n + 1 < TN) next = *(const u32x4*)(bb + (n + 1) * 16 * 128 + c0);
+#pragma unroll
+          for (int t = 0; t < TM; ++t) c[n][t] = half_mfma<IN>(b, a[t], c[n][t]);
+          b = next;
+        }
+      }
+    }
+  };
+  if (s0 < s1) issue(buf0, s0);
+  __syncthreads();
+  for (int s = s0; s < s1; s += 2) {
+    if (s + 1 < s1) issue(buf1, s + 1);
+    use(buf0);
+    __syncthreads();
+    if (s + 1 < s1) {
+      if (s + 2 < s1) issue(buf0, s + 2);
+      use(buf1);
+      __syncthreads();
+    }
+  }
+  if constexpr (WK == 2) {
+    // the second halves' sums through LDS, one column of tiles at a time in each buffer
+    static_assert(WN * WM * TM * 1024 <= (BN + BM) * 128, "");
+#pragma unroll
+    for (int n = 0; n < TN; ++n) {
+      f32x4* at = (f32x4*)(n & 1 ? buf1 : buf0) + ((wm * WN + wn) * TM) * 64 + lane;
+      if (wk == 1) {
+#pragma unroll
+        for (int t = 0; t < TM; ++t) at[t * 64] = c[n][t];
+      }
+      __syncthreads();
+      if (wk == 0) {
+#pragma unroll
+        for (int t = 0; t < TM; ++t) c[n][t] += at[t * 64];
+      }
+    }
+    __syncthreads();
+    if (wk == 1) return;
+  }
+  static_assert((WN * WM + 1) / 2 * 16 * RS * 4 <= (BN + BM) * 128, "");
+  const int at = wm * WN + wn;
+  write_tile<TN, TM>(p, c, (float*)(at & 1 ? buf1 : buf0) + (at >> 1) * 16 * RS, lane, tm0 + wm * TM * 16, tn0 + wn * TN * 16, sp);
 }
 
 // The splits' sums added in order, then the epilogue: one thread per 4 outputs.
@@ -363,7 +575,7 @@ static __global__ __launch_bounds__(256) void gemm_join_kernel(const GemmArgs p)
   if (i >= p.m) return;
   f32x4 v = {};
   for (int s = 0; s < p.nsplit; ++s) v += *(const f32x4*)(p.part + ((int64_t)s * p.m + i) * p.npad + j);
-  finish4(p, i, j, v);
+  finish4(p, i, j, v, columns_at(p, j));
 }
 
 }  // namespace mbd
