@@ -26,15 +26,15 @@ struct Tile {
   {BN, BM, WN * WM * 64, mbd::gemm_tile_lds<BN, BM>(),                                            \
    {&mbd::gemm_tile_kernel<0, BN, BM, WN, WM>, &mbd::gemm_tile_kernel<1, BN, BM, WN, WM>,         \
     &mbd::gemm_tile_kernel<2, BN, BM, WN, WM>}}
-#define DIRECT(BN, BM, WN, WM, WK, WN8, WM8)                                                            \
+#define DIRECT(BN, BM, WN, WM, WK, WN8, WM8, ST)                                                            \
   {BN, BM, WN * WM * WK * 64, 0,                                                                        \
-   {&mbd::gemm_direct_kernel<0, BN, BM, WN, WM, WK>, &mbd::gemm_direct_kernel<1, BN, BM, WN, WM, WK>,   \
-    &mbd::gemm_direct_kernel<2, BN, BM, WN8, WM8, 1>}}
+   {&mbd::gemm_direct_kernel<0, BN, BM, WN, WM, WK, ST>, &mbd::gemm_direct_kernel<1, BN, BM, WN, WM, WK, ST>,   \
+    &mbd::gemm_direct_kernel<2, BN, BM, WN8, WM8, 1, ST>}}
 // largest first; [1]: rows on 16-byte boundaries
 const Tile kTiles[2][5] = {{TILE(256, 256, 2, 4), TILE(128, 256, 2, 2), TILE(128, 128, 2, 2), TILE(64, 128, 2, 2),
                             TILE(64, 64, 2, 2)},
-                           {DIRECT(256, 256, 2, 4, 1, 2, 4), DIRECT(256, 128, 2, 2, 2, 4, 2),
-                            DIRECT(128, 128, 1, 2, 2, 2, 2), TILE(64, 128, 2, 2), TILE(64, 64, 2, 2)}};
+                           {DIRECT(256, 256, 2, 4, 1, 2, 4, 2), DIRECT(256, 128, 2, 2, 2, 4, 2, 3),
+                            DIRECT(128, 128, 1, 2, 2, 2, 2, 2), TILE(64, 128, 2, 2), TILE(64, 64, 2, 2)}};
 
 constexpr int kSkinnyWaves = 8;
 #define SKINNY(MT, U) \

@@ -122,10 +122,20 @@ __device__ __forceinline__ float activate(float y) {
   } else if constexpr (ACT == ACT_SILU) return y * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(y * -1.44269504f));
   else return y;
 }
-template <int ACT>
-__device__ __forceinline__ void activate4(float (&y)[4]) {
+template <int ACT, int N>
+__device__ __forceinline__ void activate_each(float (&y)[N]) {
 #pragma unroll
-  for (int x = 0; x < 4; ++x) y[x] = activate<ACT>(y[x]);
+  for (int x = 0; x < N; ++x) y[x] = activate<ACT>(y[x]);
+}
+template <int N>
+__device__ __forceinline__ void activate_all(float (&y)[N], int act) {
+  switch (act) {
+    case ACT_RELU: activate_each<ACT_RELU>(y); break;
+    case ACT_GELU: activate_each<ACT_GELU>(y); break;
+    case ACT_GELU_TANH: activate_each<ACT_GELU_TANH>(y); break;
+    case ACT_SILU: activate_each<ACT_SILU>(y); break;
+    default: break;
+  }
 }
 __device__ __forceinline__ void widen4(u32x2 w, int out, float (&x)[4]) {
   const uint32_t a = w[0], b = w[1];
@@ -151,7 +161,7 @@ __device__ __forceinline__ u32x2 round4(const float (&x)[4], int out) {
 }
 // 4 consecutive 16-bit values of which `left` exist (the others read as 0).
 __device__ __forceinline__ u32x2 load4(const uint16_t* p, bool whole, int left) {
-  if (whole && left >= 4) return *(const u32x2*)p;
+  if (whole && left >= 4) return *(const u32x2*)p;   // (left <= 0: nothing is read)
   uint32_t h[4];
 #pragma unroll
   for (int x = 0; x < 4; ++x) h[x] = x < left ? p[x] : 0u;
@@ -173,31 +183,51 @@ __device__ __forceinline__ Columns columns_at(const GemmArgs& p, int j) {
   if (p.bias && j < p.n) widen4(load4(p.bias + j, false, p.n - j), p.out, c.bias);
   return c;
 }
-// The epilogue of outputs j .. j+3 of token i from their sums, and their store.
-__device__ __forceinline__ void finish4(const GemmArgs& p, int64_t i, int j, f32x4 s, const Columns& c) {
-  if (i >= p.m || j >= p.n) return;
-  const float f = p.sa ? p.alpha * p.sa[i] : p.alpha;
-  float y[4], r[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-  if (p.res) widen4(load4(p.res + i * p.ldr + j, p.vec, p.n - j), p.out, r);
+// What a token's sums are multiplied by.
+__device__ __forceinline__ float token_scale(const GemmArgs& p, int64_t i) {
+  return p.sa && i < p.m ? p.alpha * p.sa[i] : p.alpha;
+}
+// The epilogue of outputs j .. j+3 of tokens i, i + step, ... from their sums
+// (times the token's scale), and their stores.  The residuals are all fetched
+// before the first store: they may be C itself, and one after another their
+// latencies would add up.
+template <int N>
+__device__ __forceinline__ void finish4(const GemmArgs& p, int64_t i, int step, int j, const f32x4 (&s)[N],
+                                        const Columns& c) {
+  u32x2 res[N];
+  if (p.res) {
 #pragma unroll
-  for (int x = 0; x < 4; ++x) y[x] = s[x] * f * c.scale[x] + c.bias[x];
-  switch (p.act) {
-    case ACT_RELU: activate4<ACT_RELU>(y); break;
-    case ACT_GELU: activate4<ACT_GELU>(y); break;
-    case ACT_GELU_TANH: activate4<ACT_GELU_TANH>(y); break;
-    case ACT_SILU: activate4<ACT_SILU>(y); break;
-    default: break;
+    for (int e = 0; e < N; ++e) {
+      const int64_t t = i + e * step;
+      res[e] = load4(p.res + t * p.ldr + j, p.vec, t < p.m ? p.n - j : 0);
+    }
   }
+  float y[4 * N];
 #pragma unroll
-  for (int x = 0; x < 4; ++x) y[x] += r[x];
-  const u32x2 o = round4(y, p.out);
-  uint16_t* to = p.C + i * p.ldc + j;
-  if (p.vec && j + 4 <= p.n) {
-    *(u32x2*)to = o;
-  } else {
+  for (int e = 0; e < N; ++e)
 #pragma unroll
-    for (int x = 0; x < 4; ++x)
-      if (j + x < p.n) to[x] = (uint16_t)(o[x >> 1] >> (16 * (x & 1)));
+    for (int x = 0; x < 4; ++x) y[4 * e + x] = __builtin_fmaf(s[e][x], c.scale[x], c.bias[x]);
+  activate_all(y, p.act);
+#pragma unroll
+  for (int e = 0; e < N; ++e) {
+    const int64_t t = i + e * step;
+    float z[4] = {y[4 * e], y[4 * e + 1], y[4 * e + 2], y[4 * e + 3]};
+    if (p.res) {
+      float r[4];
+      widen4(res[e], p.out, r);
+#pragma unroll
+      for (int x = 0; x < 4; ++x) z[x] += r[x];
+    }
+    const u32x2 o = round4(z, p.out);
+    uint16_t* to = p.C + t * p.ldc + j;
+    if (t >= p.m || j >= p.n) continue;
+    if (p.vec && j + 4 <= p.n) {
+      *(u32x2*)to = o;
+    } else {
+#pragma unroll
+      for (int x = 0; x < 4; ++x)
+        if (j + x < p.n) to[x] = (uint16_t)(o[x >> 1] >> (16 * (x & 1)));
+    }
   }
 }
 
@@ -208,26 +238,39 @@ template <int TN, int TM>
 __device__ __forceinline__ void write_tile(const GemmArgs& p, const f32x4 (&c)[TN][TM], float* mine, int lane,
                                            int row0, int col0, int sp) {
   constexpr int RS = TN * 16 + 4, LPR = TN * 4;   // floats per staged row; lanes per row
+  constexpr int STEP = 64 / LPR, NR = 16 / STEP;  // rows between a lane's, and how many it has
+  constexpr int N = NR < 4 ? NR : 4;              // of which so many at a time
   const int r = lane & 15, g = lane >> 4;
   static_assert(LPR <= 64 && 64 % LPR == 0, "a lane keeps its columns");
   const int at = (lane % LPR) * 4, j = col0 + at;
   const Columns cols = columns_at(p, j);
+  float f[TM];
+#pragma unroll
+  for (int t = 0; t < TM; ++t) f[t] = p.nsplit == 1 ? token_scale(p, row0 + t * 16 + r) : 1.0f;
 #pragma unroll 1
   for (int t = 0; t < TM; ++t) {
 #pragma unroll
     for (int tt = 0; tt < TM; ++tt)
       if (t == tt) {
 #pragma unroll
-        for (int n = 0; n < TN; ++n) *(f32x4*)(mine + r * RS + 16 * n + 4 * g) = c[n][tt];
+        for (int n = 0; n < TN; ++n) *(f32x4*)(mine + r * RS + 16 * n + 4 * g) = c[n][tt] * f[tt];
       }
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
     __builtin_amdgcn_wave_barrier();
 #pragma unroll 1
-    for (int row = lane / LPR; row < 16; row += 64 / LPR) {
-      const f32x4 v = *(const f32x4*)(mine + row * RS + at);
+    for (int row = lane / LPR; row < 16; row += N * STEP) {
+      f32x4 v[N];
+#pragma unroll
+      for (int e = 0; e < N; ++e) v[e] = *(const f32x4*)(mine + (row + e * STEP) * RS + at);
       const int i = row0 + t * 16 + row;
-      if (p.nsplit == 1) finish4(p, i, j, v, cols);
-      else if (i < p.m && j < p.npad) *(f32x4*)(p.part + ((int64_t)sp * p.m + i) * p.npad + j) = v;
+      if (p.nsplit == 1) {
+        finish4(p, i, STEP, j, v, cols);
+      } else {
+#pragma unroll
+        for (int e = 0; e < N; ++e)
+          if (i + e * STEP < p.m && j < p.npad)
+            *(f32x4*)(p.part + ((int64_t)sp * p.m + i + e * STEP) * p.npad + j) = v[e];
+      }
     }
     __builtin_amdgcn_wave_barrier();
   }
@@ -300,8 +343,10 @@ __global__ __launch_bounds__(W * 64) void gemm_skinny_kernel(const GemmArgs p) {
 #pragma unroll
     for (int w = 0; w < W; ++w) v += *(const f32x4*)&sums[w][t][l * 4];
     const int i = 16 * t + (l & 15), j = row0 + 4 * (l >> 4);
-    if (p.nsplit == 1) finish4(p, i, j, v, columns_at(p, j));
-    else if (i < p.m) *(f32x4*)(p.part + ((int64_t)sp * p.m + i) * p.npad + j) = v;
+    if (p.nsplit == 1) {
+      const f32x4 one[1] = {v * token_scale(p, i)};
+      finish4(p, i, 0, j, one, columns_at(p, j));
+    } else if (i < p.m) *(f32x4*)(p.part + ((int64_t)sp * p.m + i) * p.npad + j) = v;
   }
 }
 
@@ -421,6 +466,16 @@ __device__ __forceinline__ void load_to_lds(__amdgpu_buffer_rsrc_t r, uint8_t* t
   __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)to, 16, off, 0, 0, 0);
 }
 
+// Every wave's loads but its last N have landed, for every wave of the workgroup.
+template <int N>
+__device__ __forceinline__ void step_barrier() {
+  asm volatile("" ::: "memory");
+  // vmcnt <= N (bits 3:0 and 15:14) and lgkmcnt 0; expcnt at its maximum
+  __builtin_amdgcn_s_waitcnt((N & 15) | (7 << 4) | ((N >> 4) << 14));
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
 // ---- many tokens, rows on 16-byte boundaries ----------------------------------
 // The same tile with loads that write LDS directly (no registers, no LDS store
 // instructions), so a slab is on its way into one buffer while the other is
@@ -431,7 +486,7 @@ __device__ __forceinline__ void load_to_lds(__amdgpu_buffer_rsrc_t r, uint8_t* t
 // with one 64-byte half of every slab, and add their sums at the end -- the
 // operand traffic of 4 big wave tiles with 8 waves to hide its latency.
 
-template <int IN, int BN, int BM, int WN, int WM, int WK>
+template <int IN, int BN, int BM, int WN, int WM, int WK, int ST>
 __global__ __launch_bounds__(WN * WM * WK * 64, 2) void gemm_direct_kernel(const GemmArgs p) {
   constexpr int W = WN * WM * WK, R8 = (BN + BM) / 8, LPW = R8 / W;   // 1 KiB loads per wave and slab
   constexpr int TN = BN / WN / 16, TM = BM / WM / 16;
@@ -440,6 +495,7 @@ __global__ __launch_bounds__(WN * WM * WK * 64, 2) void gemm_direct_kernel(const
   static_assert(WK == 1 || IN != IN_E4M3, "an 8-bit instruction takes a whole slab");
   __shared__ __attribute__((aligned(16))) uint8_t buf0[(BN + BM) * 128];
   __shared__ __attribute__((aligned(16))) uint8_t buf1[(BN + BM) * 128];
+  __shared__ __attribute__((aligned(16))) uint8_t buf2[ST == 3 ? (BN + BM) * 128 : 16];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, g = lane >> 4;
   const int wn = wave % WN, wm = (wave / WN) % WM, wk = wave / (WN * WM);
@@ -502,13 +558,18 @@ __global__ __launch_bounds__(WN * WM * WK * 64, 2) void gemm_direct_kernel(const
         a[t][0] = *(const u32x4*)(ab + t * 16 * 128 + c0);
         a[t][1] = *(const u32x4*)(ab + t * 16 * 128 + c1);
       }
+      u32x4 b[2] = {*(const u32x4*)(bb + c0), *(const u32x4*)(bb + c1)};
 #pragma unroll
       for (int n = 0; n < TN; ++n) {
-        u32x4 b[2];
-        b[0] = *(const u32x4*)(bb + n * 16 * 128 + c0);
-        b[1] = *(const u32x4*)(bb + n * 16 * 128 + c1);
+        u32x4 next[2] = {b[0], b[1]};
+        if (n + 1 < TN) {
+          next[0] = *(const u32x4*)(bb + (n + 1) * 16 * 128 + c0);
+          next[1] = *(const u32x4*)(bb + (n + 1) * 16 * 128 + c1);
+        }
 #pragma unroll
         for (int t = 0; t < TM; ++t) c[n][t] = slab_mfma<IN>(b, a[t], c[n][t]);
+        b[0] = next[0];
+        b[1] = next[1];
       }
     } else {
 #pragma unroll
@@ -519,7 +580,7 @@ __global__ __launch_bounds__(WN * WM * WK * 64, 2) void gemm_direct_kernel(const
 #pragma unroll
         for (int t = 0; t < TM; ++t) a[t] = *(const u32x4*)(ab + t * 16 * 128 + c0);
         u32x4 b = *(const u32x4*)(bb + c0);
-#pragma unroll
+  #pragma unroll
         for (int n = 0; n < TN; ++n) {
           u32x4 next = b;
           if (n + 1 < TN) next = *(const u32x4*)(bb + (n + 1) * 16 * 128 + c0);
@@ -527,19 +588,39 @@ __global__ __launch_bounds__(WN * WM * WK * 64, 2) void gemm_direct_kernel(const
           for (int t = 0; t < TM; ++t) c[n][t] = half_mfma<IN>(b, a[t], c[n][t]);
           b = next;
         }
-      }
+        }
     }
   };
-  if (s0 < s1) issue(buf0, s0);
-  __syncthreads();
-  for (int s = s0; s < s1; s += 2) {
-    if (s + 1 < s1) issue(buf1, s + 1);
-    use(buf0);
+  if constexpr (ST == 2) {
+    if (s0 < s1) issue(buf0, s0);
     __syncthreads();
-    if (s + 1 < s1) {
-      if (s + 2 < s1) issue(buf0, s + 2);
-      use(buf1);
+    for (int s = s0; s < s1; s += 2) {
+      if (s + 1 < s1) issue(buf1, s + 1);
+      use(buf0);
       __syncthreads();
+      if (s + 1 < s1) {
+        if (s + 2 < s1) issue(buf0, s + 2);
+        use(buf1);
+        __syncthreads();
+      }
+    }
+  } else {
+    // Slab s + 2 is fetched while s is used: at the end of a step all but the
+    // newest slab's LPW loads have to have landed (loads into LDS keep their
+    // order; a wave's LDS reads have returned, since its products took them).
+    auto step = [&](uint8_t* far, const uint8_t* now, int s) {
+      if (s + 2 < s1) issue(far, s + 2);
+      use(now);
+      if (s + 2 < full && s + 2 < s1) step_barrier<LPW>();
+      else __syncthreads();
+    };
+    if (s0 < s1) issue(buf0, s0);
+    if (s0 + 1 < s1) issue(buf1, s0 + 1);
+    __syncthreads();
+    for (int s = s0; s < s1; s += 3) {
+      step(buf2, buf0, s);
+      if (s + 1 < s1) step(buf0, buf1, s + 1);
+      if (s + 2 < s1) step(buf1, buf2, s + 2);
     }
   }
   if constexpr (WK == 2) {
@@ -575,7 +656,8 @@ static __global__ __launch_bounds__(256) void gemm_join_kernel(const GemmArgs p)
   if (i >= p.m) return;
   f32x4 v = {};
   for (int s = 0; s < p.nsplit; ++s) v += *(const f32x4*)(p.part + ((int64_t)s * p.m + i) * p.npad + j);
-  finish4(p, i, j, v, columns_at(p, j));
+  const f32x4 one[1] = {v * token_scale(p, i)};
+  finish4(p, i, 0, j, one, columns_at(p, j));
 }
 
 }  // namespace mbd
