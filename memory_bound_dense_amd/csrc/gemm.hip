@@ -22,28 +22,32 @@ struct Tile {
   size_t lds;        // dynamic
   GemmFn fn[3];
 };
-#define TILE(BN, BM, WN, WM)                                                                      \
-  {BN, BM, WN * WM * 64, mbd::gemm_tile_lds<BN, BM>(),                                            \
-   {&mbd::gemm_tile_kernel<0, BN, BM, WN, WM>, &mbd::gemm_tile_kernel<1, BN, BM, WN, WM>,         \
-    &mbd::gemm_tile_kernel<2, BN, BM, WN, WM>}}
+#define TILE(BN, BM, WN, WM, D)                                                                     \
+  {BN, BM, WN * WM * 64, mbd::gemm_tile_lds<BN, BM>(),                                              \
+   {&mbd::gemm_tile_kernel<0, BN, BM, WN, WM, D>, &mbd::gemm_tile_kernel<1, BN, BM, WN, WM, D>,     \
+    &mbd::gemm_tile_kernel<2, BN, BM, WN, WM, D>}}
 #define DIRECT(BN, BM, WN, WM, WK, WN8, WM8, ST)                                                            \
   {BN, BM, WN * WM * WK * 64, 0,                                                                        \
    {&mbd::gemm_direct_kernel<0, BN, BM, WN, WM, WK, ST>, &mbd::gemm_direct_kernel<1, BN, BM, WN, WM, WK, ST>,   \
     &mbd::gemm_direct_kernel<2, BN, BM, WN8, WM8, 1, ST>}}
 // largest first; [1]: rows on 16-byte boundaries
-const Tile kTiles[2][5] = {{TILE(256, 256, 2, 4), TILE(128, 256, 2, 2), TILE(128, 128, 2, 2), TILE(64, 128, 2, 2),
-                            TILE(64, 64, 2, 2)},
+const Tile kTiles[2][5] = {{TILE(256, 256, 2, 4, 2), TILE(128, 256, 2, 2, 2), TILE(128, 128, 2, 2, 2),
+                            TILE(64, 128, 2, 2, 4), TILE(64, 64, 2, 2, 4)},
                            {DIRECT(256, 256, 2, 4, 1, 2, 4, 2), DIRECT(256, 128, 2, 2, 2, 4, 2, 3),
-                            DIRECT(128, 128, 1, 2, 2, 2, 2, 2), TILE(64, 128, 2, 2), TILE(64, 64, 2, 2)}};
+                            DIRECT(128, 128, 1, 2, 2, 2, 2, 2), TILE(64, 128, 2, 2, 4), TILE(64, 64, 2, 2, 4)}};
 
+// Few tokens: [row tiles 1..4][token tiles 1, 2, 4][type].
 constexpr int kSkinnyWaves = 8;
-#define SKINNY(MT, U) \
-  {&mbd::gemm_skinny_kernel<0, MT, 8, U>, &mbd::gemm_skinny_kernel<1, MT, 8, U>, &mbd::gemm_skinny_kernel<2, MT, 8, U>}
-const GemmFn kSkinny[2][3] = {SKINNY(1, 4), SKINNY(2, 2)};
+#define SKINNY(RT, MT, U) \
+  {&mbd::gemm_skinny_kernel<0, RT, MT, 8, U>, &mbd::gemm_skinny_kernel<1, RT, MT, 8, U>, &mbd::gemm_skinny_kernel<2, RT, MT, 8, U>}
+const GemmFn kSkinny[4][3][3] = {{SKINNY(1, 1, 2), SKINNY(1, 2, 2), SKINNY(1, 4, 1)},
+                                 {SKINNY(2, 1, 2), SKINNY(2, 2, 2), SKINNY(2, 4, 1)},
+                                 {SKINNY(3, 1, 2), SKINNY(3, 2, 2), SKINNY(3, 4, 1)},
+                                 {SKINNY(4, 1, 1), SKINNY(4, 2, 1), SKINNY(4, 4, 1)}};
 
 struct GemmPlan {
   const Tile* tile;  // null: skinny
-  int mt;            // skinny: token tiles
+  int rt, mt;        // skinny: row tiles, token tiles (by index)
   int64_t tiles_m, tiles_n, nsplit, npad;
   size_t bytes;
 };
@@ -53,11 +57,25 @@ GemmPlan gemm_plan(const gemm_t* p, bool whole) {
   GemmPlan g = {};
   const int64_t slabs = (p->k * in_bytes(p->in_type) + 127) / 128;
   g.nsplit = 1;
-  if (p->m <= 32) {
-    g.mt = p->m <= 16 ? 1 : 2;
+  if (p->m <= 64) {
+    // Row tiles per workgroup: whole rounds over the 256 CUs, each as long as
+    // its rows and (about 0.3 of a row tile per token tile) its tokens take.
+    // Measured, 16 tokens, 1 / 2 / 3 / 4 row tiles: n = 11008, k = 4096 19.4 /
+    // 20.4 / 17.2 / 18.0 us; n = 14336 25.4 / 22.9 / 29.0 / 22.2; n = 4096, k =
+    // 11008 20.9 / 27.0 / 32.5 / 38.8.
+    g.mt = p->m <= 16 ? 0 : p->m <= 32 ? 1 : 2;
+    const int64_t t16 = (p->n + 15) / 16;
+    int64_t best = 0;
+    for (int rt = 1; rt <= 4; ++rt) {
+      const int64_t groups = (t16 + rt - 1) / rt, cost = (groups + 255) / 256 * (10 * rt + (3 << g.mt));
+      if (rt == 1 || cost < best) {
+        best = cost;
+        g.rt = rt - 1;
+        g.tiles_n = groups;
+      }
+    }
     g.tiles_m = 1;
-    g.tiles_n = (p->n + 15) / 16;
-    const int64_t want = (256 + g.tiles_n - 1) / g.tiles_n;
+    const int64_t want = 256 / g.tiles_n;
     g.nsplit = std::max(std::min(want, slabs / (kSkinnyWaves * 2)), (int64_t)1);
   } else {
     // the largest tile that still gives every CU one
@@ -192,7 +210,7 @@ extern "C" gemv_status_t gemm_run(gemv_handle_t h, const gemm_t* p, const void* 
   if (grid > ((int64_t)1 << 31) / threads || jgrid > ((int64_t)1 << 23))
     return report(h, GEMV_ERR_TOO_LARGE, "gemm_run grid");
   void* args[] = {(void*)&a};
-  const void* fn = (const void*)(g.tile ? g.tile->fn[p->in_type] : kSkinny[g.mt - 1][p->in_type]);
+  const void* fn = (const void*)(g.tile ? g.tile->fn[p->in_type] : kSkinny[g.rt][g.mt][p->in_type]);
   hipError_t err = hipLaunchKernel(fn, dim3((unsigned)grid), dim3((unsigned)threads), args,
                                    g.tile ? g.tile->lds : 0, stream);
   if (err == hipSuccess && g.nsplit > 1)

@@ -276,91 +276,143 @@ __device__ __forceinline__ void write_tile(const GemmArgs& p, const f32x4 (&c)[T
   }
 }
 
-// ---- few tokens: B streamed once, straight into registers --------------------
-// A workgroup owns 16 rows of B and all tokens (16 MT); its W waves share the
-// slabs of k and add their sums through LDS in wave order.
+// ---- few tokens: B streamed once ----------------------------------------------
+// A workgroup owns 16 RT rows of B and all tokens (16 MT); its W waves share the
+// slabs of k and add their sums through LDS in wave order.  A wave fetches a
+// slab as 1 KiB loads of 8 rows, 8 neighbouring lanes to a row, and turns it
+// into operands through LDS of its own.  Loads that fetch operands
+// directly take 16 bytes of a different row in every lane, 64 separate lines
+// each, and stop at 3.0 TB/s whatever the depth.  U slabs are kept in flight.
 
-template <int IN, int MT, int W, int U>
+template <int IN, int RT, int MT, int W, int U>
 __global__ __launch_bounds__(W * 64) void gemm_skinny_kernel(const GemmArgs p) {
-  __shared__ __attribute__((aligned(16))) float sums[W][MT][256];
+  __shared__ __attribute__((aligned(16))) uint8_t turn[W][(RT + MT) * 2048];
+  static_assert(RT * MT * 1024 <= (RT + MT) * 2048, "a wave's sums take the place of its slabs");
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int r = lane & 15, g = lane >> 4;
+  const int r = lane & 15, g = lane >> 4, lr = lane >> 3, lc = lane & 7;
   const int64_t unit = xcd_unit(blockIdx.x, gridDim.x);
   const int sp = (int)(unit % p.nsplit);
-  const int row0 = (int)(unit / p.nsplit) * 16;
-  const int rows = min(16, p.n - row0);
+  const int row0 = (int)(unit / p.nsplit) * 16 * RT;
+  const int rows = min(16 * RT, p.n - row0);
   const __amdgpu_buffer_rsrc_t br =
       make_rsrc(p.B + (int64_t)row0 * p.ldb, (uint32_t)((int64_t)(rows - 1) * p.ldb + p.kbytes));
   const __amdgpu_buffer_rsrc_t ar = make_rsrc(p.A, (uint32_t)((int64_t)(p.m - 1) * p.lda + p.kbytes));
   // rows behind the last one are not read at all
-  const uint32_t boff = r < rows ? (uint32_t)(r * p.ldb) : kOffsetOutOfRange;
-  uint32_t aoff[MT];
+  uint32_t boff[2 * RT], aoff[MT * 2];
 #pragma unroll
-  for (int t = 0; t < MT; ++t) aoff[t] = 16 * t + r < p.m ? (uint32_t)((16 * t + r) * p.lda) : kOffsetOutOfRange;
+  for (int i = 0; i < 2 * RT; ++i) boff[i] = lr + 8 * i < rows ? (uint32_t)((lr + 8 * i) * p.ldb) + lc * 16 : kOffsetOutOfRange;
+#pragma unroll
+  for (int i = 0; i < MT * 2; ++i)
+    aoff[i] = lr + 8 * i < p.m ? (uint32_t)((lr + 8 * i) * p.lda) + lc * 16 : kOffsetOutOfRange;
+  uint8_t* mine = turn[wave];
+  // what the epilogue of this thread's outputs takes, on its way from the start
+  const int l = threadIdx.x & 63;
+  constexpr int E = (RT * MT + W - 1) / W;
+  Columns cols[E];
+  float scale[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    const int t = e * W + wave;
+    cols[e] = columns_at(p, row0 + 16 * (t / MT) + 4 * (l >> 4));
+    scale[e] = token_scale(p, 16 * (t % MT) + (l & 15));
+  }
+  const int wat = lr * 128 + (lc ^ lr) * 16;                       // rows lr, lr + 8: the same swizzle
+  const int c0 = r * 128 + (g ^ (r & 7)) * 16, c1 = r * 128 + ((4 + g) ^ (r & 7)) * 16;
 
-  f32x4 c[MT] = {};
+  f32x4 c[RT][MT] = {};
+  struct Slab {
+    u32x4 b[2 * RT], a[MT * 2];
+  };
+  auto use = [&](const Slab& s) {
+#pragma unroll
+    for (int i = 0; i < 2 * RT; ++i) *(u32x4*)(mine + i * 1024 + wat) = s.b[i];
+#pragma unroll
+    for (int i = 0; i < MT * 2; ++i) *(u32x4*)(mine + RT * 2048 + i * 1024 + wat) = s.a[i];
+    u32x4 a[MT][2];
+#pragma unroll
+    for (int t = 0; t < MT; ++t) {
+      a[t][0] = *(const u32x4*)(mine + (RT + t) * 2048 + c0);
+      a[t][1] = *(const u32x4*)(mine + (RT + t) * 2048 + c1);
+    }
+#pragma unroll
+    for (int w = 0; w < RT; ++w) {
+      const u32x4 b[2] = {*(const u32x4*)(mine + w * 2048 + c0), *(const u32x4*)(mine + w * 2048 + c1)};
+#pragma unroll
+      for (int t = 0; t < MT; ++t) c[w][t] = slab_mfma<IN>(b, a[t], c[w][t]);
+    }
+  };
   const int full = p.kbytes >> 7, rem = p.kbytes & 127;
   const int total = full + (rem != 0), share = sp * W + wave, shares = p.nsplit * W;
   const int q = total / shares, x = total % shares;
   int s = share * q + min(share, x);
   const int end = s + q + (share < x);
   const int fend = min(end, full);
+  Slab d[U];
+  auto fetch = [&](Slab& to, int at) {
+    const uint32_t o = (uint32_t)at * 128;
+#pragma unroll
+    for (int i = 0; i < 2 * RT; ++i) to.b[i] = __builtin_amdgcn_raw_buffer_load_b128(br, boff[i] + o, 0, 2);   // no reuse
+#pragma unroll
+    for (int i = 0; i < MT * 2; ++i) to.a[i] = __builtin_amdgcn_raw_buffer_load_b128(ar, aoff[i] + o, 0, 0);
+  };
+  // a ring of U slabs: each is refetched as soon as it has been used
+#pragma unroll
+  for (int u = 0; u < U; ++u)
+    if (s + u < fend) fetch(d[u], s + u);
   for (; s + U <= fend; s += U) {
-    u32x4 b[U][2], a[U][MT][2];
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const uint32_t o = (uint32_t)(s + u) * 128 + 64 * h + 16 * g;
-        b[u][h] = __builtin_amdgcn_raw_buffer_load_b128(br, boff + o, 0, 2);   // streamed: no reuse
-#pragma unroll
-        for (int t = 0; t < MT; ++t) a[u][t][h] = __builtin_amdgcn_raw_buffer_load_b128(ar, aoff[t] + o, 0, 0);
-      }
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-#pragma unroll
-      for (int t = 0; t < MT; ++t) c[t] = slab_mfma<IN>(b[u], a[u][t], c[t]);
-  }
-  for (; s < end; ++s) {
-    u32x4 b[2], a[MT][2];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const uint32_t o = (uint32_t)s * 128 + 64 * h + 16 * g;
-      const int left = p.kbytes - (int)o;
-      b[h] = load_chunk<IN>(br, boff + o, left);
-#pragma unroll
-      for (int t = 0; t < MT; ++t) a[t][h] = load_chunk<IN>(ar, aoff[t] + o, left);
+    for (int u = 0; u < U; ++u) {
+      use(d[u]);
+      if (s + U + u < fend) fetch(d[u], s + U + u);
     }
-#pragma unroll
-    for (int t = 0; t < MT; ++t) c[t] = slab_mfma<IN>(b, a[t], c[t]);
   }
 #pragma unroll
-  for (int t = 0; t < MT; ++t) *(f32x4*)&sums[wave][t][lane * 4] = c[t];
+  for (int u = 0; u < U; ++u)
+    if (s + u < fend) use(d[u]);
+  if (end > full && s <= full) {
+    Slab last;
+    const int left = rem - lc * 16;
+#pragma unroll
+    for (int i = 0; i < 2 * RT; ++i) last.b[i] = load_chunk<IN>(br, boff[i] + (uint32_t)full * 128, left);
+#pragma unroll
+    for (int i = 0; i < MT * 2; ++i) last.a[i] = load_chunk<IN>(ar, aoff[i] + (uint32_t)full * 128, left);
+    use(last);
+  }
+#pragma unroll
+  for (int w = 0; w < RT; ++w)
+#pragma unroll
+    for (int t = 0; t < MT; ++t) *(f32x4*)(mine + (w * MT + t) * 1024 + lane * 16) = c[w][t];
   __syncthreads();
-  for (int e = threadIdx.x; e < MT * 64; e += W * 64) {
-    const int t = e >> 6, l = e & 63;
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    const int t = e * W + wave;
+    if (t >= RT * MT) break;
     f32x4 v = {};
 #pragma unroll
-    for (int w = 0; w < W; ++w) v += *(const f32x4*)&sums[w][t][l * 4];
-    const int i = 16 * t + (l & 15), j = row0 + 4 * (l >> 4);
+    for (int w = 0; w < W; ++w) v += *(const f32x4*)(turn[w] + t * 1024 + l * 16);
+    const int i = 16 * (t % MT) + (l & 15), j = row0 + 16 * (t / MT) + 4 * (l >> 4);
     if (p.nsplit == 1) {
-      const f32x4 one[1] = {v * token_scale(p, i)};
-      finish4(p, i, 0, j, one, columns_at(p, j));
-    } else if (i < p.m) *(f32x4*)(p.part + ((int64_t)sp * p.m + i) * p.npad + j) = v;
+      const f32x4 one[1] = {v * scale[e]};
+      finish4(p, i, 0, j, one, cols[e]);
+    } else if (i < p.m && j < p.npad) {
+      *(f32x4*)(p.part + ((int64_t)sp * p.m + i) * p.npad + j) = v;
+    }
   }
 }
 
 // ---- many tokens: tiles through LDS -----------------------------------------
 // A workgroup owns BN rows of B x BM tokens; its waves are a WN x WM grid.
-// Slabs are fetched into registers two ahead and staged through two LDS
-// buffers, one barrier per slab.  A row's 16-byte chunk c lies at c ^ (row & 7),
+// Slabs are fetched into a ring of D register sets and staged through two LDS
+// buffers, one barrier per slab; D - 1 slabs are in flight.  A row's 16-byte chunk c lies at c ^ (row & 7),
 // which spreads the 16 rows that a read touches over all banks.
 
 template <int BN, int BM>
 constexpr size_t gemm_tile_lds() { return (size_t)2 * (BN + BM) * 128; }
 
-template <int IN, int BN, int BM, int WN, int WM>
-__global__ __launch_bounds__(WN * WM * 64, (WN * WM > 4 ? 2 : 1)) void gemm_tile_kernel(const GemmArgs p) {
+template <int IN, int BN, int BM, int WN, int WM, int D>
+__global__ __launch_bounds__(WN * WM * 64, (WN * WM > 4 || BN * BM <= 128 * 128 ? 2 : 1)) void gemm_tile_kernel(
+    const GemmArgs p) {
+  static_assert(D % 2 == 0, "the LDS buffer of a ring's slab is fixed");
   constexpr int T = WN * WM * 64, RPT = T / 8;           // threads; rows per load pass
   constexpr int LB = BN / RPT, LA = BM / RPT;            // passes
   constexpr int TN = BN / WN / 16, TM = BM / WM / 16;    // a wave's tiles
@@ -398,46 +450,52 @@ __global__ __launch_bounds__(WN * WM * 64, (WN * WM > 4 ? 2 : 1)) void gemm_tile
   const int q = total / p.nsplit, x = total % p.nsplit;
   const int s0 = sp * q + min(sp, x), s1 = s0 + q + (sp < x);
 
-  u32x4 fb[LB], fa[LA];
-  auto fetch = [&](int s) {
+  struct Slab {
+    u32x4 b[LB], a[LA];
+  };
+  auto fetch = [&](Slab& to, int s) {
     const uint32_t o = (uint32_t)s * 128;
     if (s < full) {
 #pragma unroll
-      for (int i = 0; i < LB; ++i) fb[i] = __builtin_amdgcn_raw_buffer_load_b128(br, bo[i] + o, 0, 0);
+      for (int i = 0; i < LB; ++i) to.b[i] = __builtin_amdgcn_raw_buffer_load_b128(br, bo[i] + o, 0, 0);
 #pragma unroll
-      for (int i = 0; i < LA; ++i) fa[i] = __builtin_amdgcn_raw_buffer_load_b128(ar, ao[i] + o, 0, 0);
+      for (int i = 0; i < LA; ++i) to.a[i] = __builtin_amdgcn_raw_buffer_load_b128(ar, ao[i] + o, 0, 0);
     } else {
       const int left = p.kbytes - (int)o - lc * 16;
 #pragma unroll
-      for (int i = 0; i < LB; ++i) fb[i] = load_chunk<IN>(br, bo[i] + o, left);
+      for (int i = 0; i < LB; ++i) to.b[i] = load_chunk<IN>(br, bo[i] + o, left);
 #pragma unroll
-      for (int i = 0; i < LA; ++i) fa[i] = load_chunk<IN>(ar, ao[i] + o, left);
+      for (int i = 0; i < LA; ++i) to.a[i] = load_chunk<IN>(ar, ao[i] + o, left);
     }
   };
-  auto place = [&](int buf) {
+  auto place = [&](const Slab& from, int buf) {
     uint8_t* b = smem + buf * (BN + BM) * 128;
 #pragma unroll
     for (int i = 0; i < LB; ++i) {
       const int row = lr + i * RPT;
-      *(u32x4*)(b + row * 128 + ((lc ^ (row & 7)) * 16)) = fb[i];
+      *(u32x4*)(b + row * 128 + ((lc ^ (row & 7)) * 16)) = from.b[i];
     }
 #pragma unroll
     for (int i = 0; i < LA; ++i) {
       const int row = lr + i * RPT;
-      *(u32x4*)(b + (BN + row) * 128 + ((lc ^ (row & 7)) * 16)) = fa[i];
+      *(u32x4*)(b + (BN + row) * 128 + ((lc ^ (row & 7)) * 16)) = from.a[i];
     }
   };
 
   f32x4 c[TN][TM] = {};
-  if (s0 < s1) {
-    fetch(s0);
-    place(s0 & 1);
-    if (s0 + 1 < s1) fetch(s0 + 1);
-    __syncthreads();
-    for (int s = s0; s < s1; ++s) {
-      if (s + 1 < s1) place((s + 1) & 1);
-      if (s + 2 < s1) fetch(s + 2);
-      const uint8_t* base = smem + (s & 1) * (BN + BM) * 128;
+  Slab ring[D];
+#pragma unroll
+  for (int u = 0; u < D; ++u)
+    if (s0 + u < s1) fetch(ring[u], s0 + u);
+  if (s0 < s1) place(ring[0], 0);
+  __syncthreads();
+  for (int s = s0; s < s1; s += D) {
+#pragma unroll
+    for (int u = 0; u < D; ++u) {
+      if (s + u >= s1) break;
+      if (s + u + 1 < s1) place(ring[(u + 1) % D], (u + 1) & 1);
+      if (s + u + D < s1) fetch(ring[u], s + u + D);
+      const uint8_t* base = smem + (u & 1) * (BN + BM) * 128;
       const uint8_t* bb = base + (wn * TN * 16 + r) * 128;
       const uint8_t* ab = base + (BN + wm * TM * 16 + r) * 128;
       const int c0 = (g ^ (r & 7)) * 16, c1 = ((4 + g) ^ (r & 7)) * 16;
