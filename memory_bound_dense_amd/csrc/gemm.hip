@@ -16,25 +16,32 @@ int64_t up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
 
 using GemmFn = void (*)(const mbd::GemmArgs);
 
-// Tiles: rows of B x tokens.
+// Tiles: rows of B x tokens, and what a slab costs, in ns: `alone` for one
+// workgroup on a CU, `shared` per workgroup where the CU has more to do.
+// Measured (bf16): the tile's time over whole rounds, e.g. aligned 256 x 256
+// 94 us for 64 slabs on 86 CUs and 98 us on 256; 128 x 128 52 us for 64 slabs
+// on 256 CUs, 116 us for 4 workgroups a CU; 64 x 64 30 us for 64 slabs, 190 us
+// for 16 a CU.
 struct Tile {
   int bn, bm, threads;
   size_t lds;        // dynamic
+  int alone, shared;
   GemmFn fn[3];
 };
-#define TILE(BN, BM, WN, WM, D)                                                                     \
-  {BN, BM, WN * WM * 64, mbd::gemm_tile_lds<BN, BM>(),                                              \
-   {&mbd::gemm_tile_kernel<0, BN, BM, WN, WM, D>, &mbd::gemm_tile_kernel<1, BN, BM, WN, WM, D>,     \
-    &mbd::gemm_tile_kernel<2, BN, BM, WN, WM, D>}}
-#define DIRECT(BN, BM, WN, WM, WK, WN8, WM8, ST)                                                            \
-  {BN, BM, WN * WM * WK * 64, 0,                                                                        \
+#define TILE(BN, BM, WN, WM, ALONE, SHARED)                                                         \
+  {BN, BM, WN * WM * 64, mbd::gemm_tile_lds<BN, BM>(), ALONE, SHARED,                               \
+   {&mbd::gemm_tile_kernel<0, BN, BM, WN, WM>, &mbd::gemm_tile_kernel<1, BN, BM, WN, WM>,           \
+    &mbd::gemm_tile_kernel<2, BN, BM, WN, WM>}}
+#define DIRECT(BN, BM, WN, WM, WK, WN8, WM8, ST, ALONE, SHARED)                                                 \
+  {BN, BM, WN * WM * WK * 64, 0, ALONE, SHARED,                                                                 \
    {&mbd::gemm_direct_kernel<0, BN, BM, WN, WM, WK, ST>, &mbd::gemm_direct_kernel<1, BN, BM, WN, WM, WK, ST>,   \
     &mbd::gemm_direct_kernel<2, BN, BM, WN8, WM8, 1, ST>}}
-// largest first; [1]: rows on 16-byte boundaries
-const Tile kTiles[2][5] = {{TILE(256, 256, 2, 4, 2), TILE(128, 256, 2, 2, 2), TILE(128, 128, 2, 2, 2),
-                            TILE(64, 128, 2, 2, 4), TILE(64, 64, 2, 2, 4)},
-                           {DIRECT(256, 256, 2, 4, 1, 2, 4, 2), DIRECT(256, 128, 2, 2, 2, 4, 2, 3),
-                            DIRECT(128, 128, 1, 2, 2, 2, 2, 2), TILE(64, 128, 2, 2, 4), TILE(64, 64, 2, 2, 4)}};
+// [1]: rows on 16-byte boundaries
+const Tile kTiles[2][5] = {
+    {TILE(256, 256, 2, 4, 2300, 2300), TILE(128, 128, 2, 2, 1070, 750), TILE(64, 128, 2, 2, 850, 500),
+     TILE(64, 64, 2, 2, 520, 330), {}},
+    {DIRECT(256, 256, 2, 4, 1, 2, 4, 2, 1470, 1470), DIRECT(256, 128, 2, 2, 2, 4, 2, 3, 920, 920),
+     DIRECT(128, 128, 1, 2, 2, 2, 2, 2, 810, 470), TILE(64, 128, 2, 2, 580, 350), TILE(64, 64, 2, 2, 470, 190)}};
 
 // Few tokens: [row tiles 1..4][token tiles 1, 2, 4][type].
 constexpr int kSkinnyWaves = 8;
@@ -78,15 +85,27 @@ GemmPlan gemm_plan(const gemm_t* p, bool whole) {
     const int64_t want = 256 / g.tiles_n;
     g.nsplit = std::max(std::min(want, slabs / (kSkinnyWaves * 2)), (int64_t)1);
   } else {
-    // the largest tile that still gives every CU one
+    // The tile and the split of k with the least modelled time: a CU's share of
+    // the slabs, and for a split the partial sums' way through memory (4 TB/s)
+    // and a second launch (4 us).
+    int64_t best = 0;
     for (const Tile& t : kTiles[whole]) {
-      g.tile = &t;
-      if (((p->m + t.bm - 1) / t.bm) * ((p->n + t.bn - 1) / t.bn) >= 256) break;
+      if (!t.bn) continue;
+      const int64_t tm = (p->m + t.bm - 1) / t.bm, tn = (p->n + t.bn - 1) / t.bn;
+      for (int64_t ns = 1; ns <= 8; ++ns) {
+        if (ns > 1 && slabs / ns < 4) break;
+        const int64_t rounds = (tm * tn * ns + 255) / 256;
+        int64_t cost = (slabs + ns - 1) / ns * std::max((int64_t)t.alone, rounds * t.shared);
+        if (ns > 1) cost += 4000 + ns * p->m * p->n / 500;
+        if (!g.tile || cost < best) {
+          best = cost;
+          g.tile = &t;
+          g.tiles_m = tm;
+          g.tiles_n = tn;
+          g.nsplit = ns;
+        }
+      }
     }
-    g.tiles_m = (p->m + g.tile->bm - 1) / g.tile->bm;
-    g.tiles_n = (p->n + g.tile->bn - 1) / g.tile->bn;
-    const int64_t want = 256 / (g.tiles_m * g.tiles_n);
-    g.nsplit = std::max(std::min(want, slabs / 8), (int64_t)1);
   }
   g.npad = up(p->n, 4);
   if (!g.tile) g.npad = up(p->n, 16);
@@ -150,7 +169,7 @@ bool mbd_host::gemm_set_attributes() {
   for (const auto& set : kTiles)
     for (const Tile& t : set)
       for (GemmFn f : t.fn)
-        if (t.lds &&
+        if (f && t.lds &&
             hipFuncSetAttribute((const void*)f, hipFuncAttributeMaxDynamicSharedMemorySize, (int)t.lds) != hipSuccess)
           return false;
   return true;

@@ -402,17 +402,17 @@ __global__ __launch_bounds__(W * 64) void gemm_skinny_kernel(const GemmArgs p) {
 
 // ---- many tokens: tiles through LDS -----------------------------------------
 // A workgroup owns BN rows of B x BM tokens; its waves are a WN x WM grid.
-// Slabs are fetched into a ring of D register sets and staged through two LDS
-// buffers, one barrier per slab; D - 1 slabs are in flight.  A row's 16-byte chunk c lies at c ^ (row & 7),
+// Slabs are fetched into two register sets in turn and staged through two LDS
+// buffers, one barrier per slab.  A row's 16-byte chunk c lies at c ^ (row & 7),
 // which spreads the 16 rows that a read touches over all banks.
 
 template <int BN, int BM>
 constexpr size_t gemm_tile_lds() { return (size_t)2 * (BN + BM) * 128; }
 
-template <int IN, int BN, int BM, int WN, int WM, int D>
+template <int IN, int BN, int BM, int WN, int WM>
 __global__ __launch_bounds__(WN * WM * 64, (WN * WM > 4 || BN * BM <= 128 * 128 ? 2 : 1)) void gemm_tile_kernel(
     const GemmArgs p) {
-  static_assert(D % 2 == 0, "the LDS buffer of a ring's slab is fixed");
+  constexpr int D = 2;
   constexpr int T = WN * WM * 64, RPT = T / 8;           // threads; rows per load pass
   constexpr int LB = BN / RPT, LA = BM / RPT;            // passes
   constexpr int TN = BN / WN / 16, TM = BM / WM / 16;    // a wave's tiles

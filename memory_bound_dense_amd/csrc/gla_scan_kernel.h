@@ -460,6 +460,33 @@ __device__ __forceinline__ void step_gates(const Step& t, const uint32_t (&gw)[k
   make_gates<DT, G32, REV>(w, lane, q);
 }
 
+// The scores of a step are shared: each of the NW waves computes 4 / NW of the
+// four 16 x 16 tiles (rows j of tile jt, columns i of tile it), drops what lies
+// behind the diagonal and leaves its bf16 terms where the product over j reads
+// them: [it][term][lane], a lane's 8 positions j being rows 4g..4g+3 of both jt.
+template <int NW> constexpr int kMine = 4 / NW;
+template <int NW>
+__device__ __forceinline__ void score_tile(int wave, int i, int& jt, int& it) {
+  jt = NW == 4 ? wave & 1 : i;
+  it = NW == 4 ? wave >> 1 : wave;
+}
+template <int TERMS>
+__device__ __forceinline__ void put_scores(uint8_t* ps, f32x4 x, int jt, int it, int lane) {
+  const int n = lane & 15, g = lane >> 4;
+#pragma unroll
+  for (int r = 0; r < 4; ++r) x[r] = 8 * g + 4 * jt + r <= row_of(n, it) ? x[r] : 0.0f;
+  uint32_t a[TERMS], b[TERMS];
+  split2<TERMS>(x[0], x[1], a);
+  split2<TERMS>(x[2], x[3], b);
+#pragma unroll
+  for (int m = 0; m < TERMS; ++m) *(u32x2*)(ps + ((it * TERMS + m) * 64 + lane) * 16 + 8 * jt) = u32x2{a[m], b[m]};
+}
+template <int TERMS>
+__device__ __forceinline__ void get_scores(const uint8_t* ps, int it, int lane, bf16x8 (&x)[TERMS]) {
+#pragma unroll
+  for (int m = 0; m < TERMS; ++m) x[m] = *(const bf16x8*)(ps + ((it * TERMS + m) * 64 + lane) * 16);
+}
+
 // ---- out_i = X_i^T S ---------------------------------------------------------
 // A wave owns 32 columns of the state (64 VGPRs at DK 128) and of the output;
 // X e^{G-r} and K e^{r-G} are computed once per workgroup, 32 channels per
@@ -468,7 +495,7 @@ __device__ __forceinline__ void step_gates(const Step& t, const uint32_t (&gw)[k
 template <int NS>
 constexpr size_t scan_out_lds() {
   return (size_t)4 * kScanC * (NS * 32 + kPadRow) * 2 + (size_t)3 * NS * 32 * kTokRow * 2 +
-         (size_t)NS * 32 * 4 + 64;
+         (size_t)NS * 32 * 4 + 4096 + 64;
 }
 
 template <int DT, bool G32, int NS, int NW, bool REV>
@@ -481,7 +508,8 @@ __global__ __launch_bounds__(NW * 64, NS > 4 ? 1 : 2) void scan_out_kernel(const
   uint16_t* ks = xs + 2 * kScanC * RS;                // K e^{r-G}: 2 terms of [32][RS]
   uint16_t* kt = ks + 2 * kScanC * RS;                // the same, 3 terms of [DKP][kTokRow]
   float* dec = (float*)(kt + 3 * DKP * kTokRow);      // the state's decay before the step, [DKP]
-  int* wild = (int*)(dec + DKP);                  // one flag per wave
+  uint8_t* sc = (uint8_t*)(dec + DKP);                // the scores' terms
+  int* wild = (int*)(sc + 4096);                      // one flag per wave
 
   Place p;
   if (!place_of(a, p)) return;
@@ -638,21 +666,26 @@ __global__ __launch_bounds__(NW * 64, NS > 4 ? 1 : 2) void scan_out_kernel(const
       if (next < nch) fetch(next);   // in flight during the products
     }
     f32x4 o[2][2] = {};
-    f32x4 pt[2][2] = {};   // scores, transposed: rows j, columns i
+    f32x4 pt[kMine<NW>] = {};   // this wave's scores, transposed: rows j, columns i
 #pragma unroll
     for (int s = 0; s < NS; ++s) {
-      bf16x8 kk[2][2], xx[2][2];
+      bf16x8 xx[2][2];
 #pragma unroll
       for (int tl = 0; tl < 2; ++tl)
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          kk[tl][i] = *(const bf16x8*)(ks + (i * kScanC + row_of(n, tl)) * RS + 32 * s + 8 * g);
+        for (int i = 0; i < 2; ++i)
           xx[tl][i] = *(const bf16x8*)(xs + (i * kScanC + row_of(n, tl)) * RS + 32 * s + 8 * g);
-        }
 #pragma unroll
-      for (int jt = 0; jt < 2; ++jt)
+      for (int m = 0; m < kMine<NW>; ++m) {
+        int jt, it;
+        score_tile<NW>(wave, m, jt, it);
+        bf16x8 kk[2];
 #pragma unroll
-        for (int it = 0; it < 2; ++it) pt[jt][it] = mfma_terms<2, 2>(kk[jt], xx[it], pt[jt][it]);
+        for (int i = 0; i < 2; ++i)
+          kk[i] = *(const bf16x8*)(ks + (i * kScanC + row_of(n, jt)) * RS + 32 * s + 8 * g);
+        if (it) pt[m] = mfma_terms<2, 2>(kk, xx[1], pt[m]);
+        else pt[m] = mfma_terms<2, 2>(kk, xx[0], pt[m]);
+      }
       f32x4 d0 = *(const f32x4*)(dec + 32 * s + 8 * g), d1 = *(const f32x4*)(dec + 32 * s + 8 * g + 4);
 #pragma unroll
       for (int nt = 0; nt < 2; ++nt) {
@@ -670,21 +703,15 @@ __global__ __launch_bounds__(NW * 64, NS > 4 ? 1 : 2) void scan_out_kernel(const
         for (int it = 0; it < 2; ++it) o[it][nt] = mfma_terms<2, 2>(xx[it], sx, o[it][nt]);
       }
     }
+#pragma unroll
+    for (int m = 0; m < kMine<NW>; ++m) {
+      int jt, it;
+      score_tile<NW>(wave, m, jt, it);
+      put_scores<2>(sc, pt[m], jt, it, lane);
+    }
     bf16x8 vt[2][kTerms<DT>];
     exact_terms<DT>(vc[0], vt[0]);
     exact_terms<DT>(vc[1], vt[1]);
-#pragma unroll
-    for (int it = 0; it < 2; ++it) {
-      float x[8];
-#pragma unroll
-      for (int jt = 0; jt < 2; ++jt)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) x[4 * jt + r] = 8 * g + 4 * jt + r <= row_of(n, it) ? pt[jt][it][r] : 0.0f;
-      bf16x8 ps[2];
-      split8<2>(x, ps);
-#pragma unroll
-      for (int nt = 0; nt < 2; ++nt) o[it][nt] = mfma_terms(ps, vt[nt], o[it][nt]);
-    }
 #pragma unroll
     for (int s = 0; s < NS; ++s)
 #pragma unroll
@@ -696,6 +723,16 @@ __global__ __launch_bounds__(NW * 64, NS > 4 ? 1 : 2) void scan_out_kernel(const
 #pragma unroll
         for (int nt = 0; nt < 2; ++nt) S[s][tl][nt] = mfma_terms(kk, vt[nt], S[s][tl][nt]);
       }
+    // from here on the next step may be staged: only the scores are still read,
+    // and they are written again behind its own barrier
+    __syncthreads();
+#pragma unroll
+    for (int it = 0; it < 2; ++it) {
+      bf16x8 ps[2];
+      get_scores<2>(sc, it, lane, ps);
+#pragma unroll
+      for (int nt = 0; nt < 2; ++nt) o[it][nt] = mfma_terms(ps, vt[nt], o[it][nt]);
+    }
     const __amdgpu_buffer_rsrc_t orsrc = chunk_rsrc(a.O, ob, nv, a.dv, 2);
     const Lane ot = fresh(ol);
 #pragma unroll
@@ -705,7 +742,6 @@ __global__ __launch_bounds__(NW * 64, NS > 4 ? 1 : 2) void scan_out_kernel(const
                      pair_round<DT>(o[j >> 2][0][j & 3] * a.oscale, o[j >> 2][1][j & 3] * a.oscale));
     if (next != c) walk<REV>(a.O, ob, 2);
     c = next;
-    __syncthreads();
   }
 
   if (a.ST && (REV ? p.seg == 0 : p.last)) {
@@ -740,7 +776,7 @@ __global__ __launch_bounds__(NW * 64, NS > 4 ? 1 : 2) void scan_out_kernel(const
 
 template <int NV>
 constexpr size_t scan_grad_lds() {
-  return (size_t)2 * kScanC * (NV * 32 + kPadRow) * 2 + (size_t)NV * 32 * kTokRow * 2 + 64;
+  return (size_t)2 * kScanC * (NV * 32 + kPadRow) * 2 + (size_t)NV * 32 * kTokRow * 2 + 6144 + 64;
 }
 
 template <int DT, bool G32, int NV, int NW, bool REV, bool GRAD>
@@ -755,7 +791,8 @@ __global__ __launch_bounds__(NW * 64, NV > 4 ? 1 : 2) void scan_grad_kernel(cons
   uint16_t* vs = (uint16_t*)smem;               // V [32][RS]
   uint16_t* ws = vs + kScanC * RS;              // W [32][RS]
   uint16_t* vt = ws + kScanC * RS;              // V transposed [DVP][kTokRow]
-  int* wild = (int*)(vt + DVP * kTokRow);
+  uint8_t* sc = (uint8_t*)(vt + DVP * kTokRow);   // the scores' terms
+  int* wild = (int*)(sc + 6144);
 
   Place p;
   if (!place_of(a, p)) return;
@@ -921,28 +958,28 @@ __global__ __launch_bounds__(NW * 64, NV > 4 ? 1 : 2) void scan_grad_kernel(cons
       st = Step{0, 32};
       if (next < nch) fetch(next);   // in flight during the products
     }
+    f32x4 o[2][2] = {};
     if (GRAD) {
-      f32x4 o[2][2] = {};
-      f32x4 pt[2][2] = {};   // W_i . V_j, rows j, columns i
+      f32x4 pt[kMine<NW>] = {};   // this wave's W_i . V_j: rows j, columns i
 #pragma unroll
       for (int s = 0; s < NV; ++s) {
-        u32x4 vv[2], wr[2];
+        u32x4 wr[2];
         bf16x8 wt[2][kTerms<DT>];
 #pragma unroll
         for (int tl = 0; tl < 2; ++tl) {
-          vv[tl] = *(const u32x4*)(vs + row_of(n, tl) * RS + 32 * s + 8 * g);
           wr[tl] = *(const u32x4*)(ws + row_of(n, tl) * RS + 32 * s + 8 * g);
           exact_terms<DT>(wr[tl], wt[tl]);
         }
 #pragma unroll
-        for (int jt = 0; jt < 2; ++jt)
-#pragma unroll
-          for (int it = 0; it < 2; ++it) {
-            if constexpr (DT == DT_F16)
-              pt[jt][it] = mfma(__builtin_bit_cast(f16x8, vv[jt]), __builtin_bit_cast(f16x8, wr[it]), pt[jt][it]);
-            else
-              pt[jt][it] = mfma(__builtin_bit_cast(bf16x8, vv[jt]), wt[it][0], pt[jt][it]);
-          }
+        for (int m = 0; m < kMine<NW>; ++m) {
+          int jt, it;
+          score_tile<NW>(wave, m, jt, it);
+          const u32x4 vv = *(const u32x4*)(vs + row_of(n, jt) * RS + 32 * s + 8 * g), wv = it ? wr[1] : wr[0];
+          if constexpr (DT == DT_F16)
+            pt[m] = mfma(__builtin_bit_cast(f16x8, vv), __builtin_bit_cast(f16x8, wv), pt[m]);
+          else
+            pt[m] = mfma(__builtin_bit_cast(bf16x8, vv), __builtin_bit_cast(bf16x8, wv), pt[m]);
+        }
 #pragma unroll
         for (int nt = 0; nt < 2; ++nt) {
           float x[8];
@@ -960,14 +997,36 @@ __global__ __launch_bounds__(NW * 64, NV > 4 ? 1 : 2) void scan_grad_kernel(cons
         }
       }
 #pragma unroll
+      for (int m = 0; m < kMine<NW>; ++m) {
+        int jt, it;
+        score_tile<NW>(wave, m, jt, it);
+        put_scores<TP>(sc, pt[m], jt, it, lane);
+      }
+    } else {
+#pragma unroll
+      for (int s = 0; s < NV; ++s)
+#pragma unroll
+        for (int tl = 0; tl < 2; ++tl)
+#pragma unroll
+          for (int nt = 0; nt < 2; ++nt) S[s][tl][nt] *= q.a[nt];
+    }
+#pragma unroll
+    for (int s = 0; s < NV; ++s)
+#pragma unroll
+      for (int tl = 0; tl < 2; ++tl) {
+        bf16x8 vv[kTerms<DT>];
+        exact_terms<DT>(*(const u32x4*)(vt + (32 * s + row_of(n, tl)) * kTokRow + 8 * g), vv);
+#pragma unroll
+        for (int nt = 0; nt < 2; ++nt) S[s][tl][nt] = mfma_terms(vv, kk[nt], S[s][tl][nt]);
+      }
+    // from here on the next step may be staged: only the scores are still read,
+    // and they are written again behind its own barrier
+    __syncthreads();
+    if (GRAD) {
+#pragma unroll
       for (int it = 0; it < 2; ++it) {
-        float x[8];
-#pragma unroll
-        for (int jt = 0; jt < 2; ++jt)
-#pragma unroll
-          for (int r = 0; r < 4; ++r) x[4 * jt + r] = 8 * g + 4 * jt + r <= row_of(n, it) ? pt[jt][it][r] : 0.0f;
         bf16x8 ps[TP];
-        split8<TP>(x, ps);
+        get_scores<TP>(sc, it, lane, ps);
 #pragma unroll
         for (int nt = 0; nt < 2; ++nt) {
           if constexpr (TP == 3) {
@@ -1041,30 +1100,13 @@ __global__ __launch_bounds__(NW * 64, NV > 4 ? 1 : 2) void scan_grad_kernel(cons
           }
         }
       }
-    } else {
-#pragma unroll
-      for (int s = 0; s < NV; ++s)
-#pragma unroll
-        for (int tl = 0; tl < 2; ++tl)
-#pragma unroll
-          for (int nt = 0; nt < 2; ++nt) S[s][tl][nt] *= q.a[nt];
     }
-#pragma unroll
-    for (int s = 0; s < NV; ++s)
-#pragma unroll
-      for (int tl = 0; tl < 2; ++tl) {
-        bf16x8 vv[kTerms<DT>];
-        exact_terms<DT>(*(const u32x4*)(vt + (32 * s + row_of(n, tl)) * kTokRow + 8 * g), vv);
-#pragma unroll
-        for (int nt = 0; nt < 2; ++nt) S[s][tl][nt] = mfma_terms(vv, kk[nt], S[s][tl][nt]);
-      }
     if (GRAD && next != c) {
       walk<REV>(a.X, xb, 2);
       walk<REV>(a.O, ob, 2);
       if (REV) walk<REV>(a.DG, dgb, gb);
     }
     c = next;
-    __syncthreads();
   }
 
   // the last step's second half
