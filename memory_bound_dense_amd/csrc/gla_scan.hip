@@ -84,17 +84,25 @@ int out_cols(int64_t dv) {   // output columns per workgroup: even shares of at 
 }
 
 // Sequences are cut into segments that run side by side when the heads alone
-// leave the GPU's 256 CUs (two workgroups each) idle.
+// leave the GPU idle: as many as fit it in one round (two workgroups of four
+// waves a CU, or four of two; a few more than that take a second round: 156
+// heads and blocks in 4 segments of 400 tokens 173 us, in 3 127), of at least
+// 64 tokens (forward; the segments' own states are a pass of their own) or 32
+// (backward).  Measured forward, 32 heads of 128 x 128, 512 tokens: segments of
+// 64 / 128 / 256 tokens 48 / 59 / 79 us; 129 tokens: whole 32 us, in segments of
+// 64 or 96 39..43.  Backward, 15 heads of 64 x 96, 1001 tokens: segments of 32 /
+// 64 / 160 / 256 tokens 113 / 136 / 187 / 344 us.
 ScanPlan scan_plan(const gla_scan_t* p, bool backward) {
   ScanPlan s = {};
   s.dkp = (int32_t)up(p->dk, 32);
   s.dvp = (int32_t)up(p->dv, 32);
   s.heads = p->batch * p->heads;
-  const int64_t blocks = backward ? (p->dk + 127) / 128 : (p->dv + out_cols(p->dv) - 1) / out_cols(p->dv);
-  const int64_t units = s.heads * blocks;
-  constexpr int64_t kUnits = 512, kMinTokens = 128;
-  int64_t nseg = units > 0 ? (kUnits + units - 1) / units : 1;
-  nseg = std::min(nseg, p->tokens / kMinTokens);
+  const int64_t width = backward ? p->dk : out_cols(p->dv);
+  const int waves = waves_of(width);
+  const int64_t blocks = backward ? (p->dk + 32 * waves - 1) / (32 * waves) : (p->dv + width - 1) / width;
+  const int64_t room = 2048 / waves / std::max(s.heads * blocks, (int64_t)1);
+  int64_t nseg = std::min(room, p->tokens / (backward ? 32 : 64));
+  if (p->tokens < (backward ? 128 : 256)) nseg = 1;
   nseg = std::max(nseg, (int64_t)1);
   const int64_t L = std::max(up((p->tokens + nseg - 1) / nseg, mbd::kScanC), (int64_t)mbd::kScanC);
   s.L = (int)L;
