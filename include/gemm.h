@@ -33,8 +33,9 @@
  * scratch: gemm_workspace_bytes says how much (possibly 0), any contents,
  * 16-byte aligned, not shared by calls that can overlap on the GPU.
  *
- * Limits (GEMV_ERR_TOO_LARGE): m, n <= 2^30; lda and ldb at most 2^23 bytes,
- * ldc and ldr at most 2^30 elements.
+ * Limits (GEMV_ERR_TOO_LARGE): m, n, k <= 2^30; lda and ldb at most 2^23 bytes,
+ * ldc and ldr at most 2^30 elements; gemm_run also where the tiles it picks are
+ * more than a launch takes (beyond 2^36 outputs at the least).
  */
 #ifndef MBD_GEMM_H
 #define MBD_GEMM_H

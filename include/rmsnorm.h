@@ -24,7 +24,7 @@
  *
  * Like gemv_run: host validation, one kernel enqueued on `stream`, no
  * allocation, no synchronisation; on any error nothing is launched.  m == 0
- * or n == 0 is a no-op.  Limits (GEMV_ERR_TOO_LARGE): m <= 2^22, n <= 2^24,
+ * or n == 0 is a no-op.  Limits (GEMV_ERR_TOO_LARGE): m <= 2^21, n <= 2^24,
  * leading dimensions <= 2^30.
  */
 #ifndef MBD_RMSNORM_H

@@ -233,7 +233,7 @@ extern "C" gemv_status_t rmsnorm_check_args(const rmsnorm_t* p, const void* x, c
   if (p->m < 0 || p->n < 0) return GEMV_ERR_INVALID_ARG;
   if (p->m == 0 || p->n == 0) return GEMV_OK;
   const int64_t lim = (int64_t)1 << 30;
-  if (p->m > ((int64_t)1 << 22) || p->n > ((int64_t)1 << 24) || p->ldx > lim || p->ldy > lim ||
+  if (p->m > ((int64_t)1 << 21) || p->n > ((int64_t)1 << 24) || p->ldx > lim || p->ldy > lim ||
       (residual && p->ldres > lim) || (sum_out && p->ldsum > lim))
     return GEMV_ERR_TOO_LARGE;
   if (p->ldx < p->n || p->ldy < p->n || (residual && p->ldres < p->n) || (sum_out && p->ldsum < p->n))
