@@ -186,20 +186,31 @@ def test_nothing_leaks_from_other_tokens(scan, what, value, t):
     for n in ("dq", "dk", "dv", "dg"):
         assert torch.equal(r[n][:, :, 1], clean[n][:, :, 1]), n
     assert torch.equal(ST[:, 1], clean_S[:, 1])
-    e = U * 2 ** 12      # chunk boundaries may fall into other steps: only rounding may differ
-    near = lambda a, b: torch.allclose(a.float(), b.float(), rtol=2 ** -7, atol=e)
+    # the token's chunk is taken in other steps, so only rounding may differ: both runs are
+    # within the bound and one half step of the same exact value
+    y = inputs(1, t, 2, 64, 64, BF, BF, gate=16.0, state=False)
+    a = [f64(y[n][0]) for n in ("q", "k", "v", "g", "do")]
+    ab = scan_ref.backward(*a, y["scale"])[1]
+    ab["o"] = scan_ref.forward(*a[:4], y["scale"])[2]
+    rel = scan_ref.rel16(t, a[3])
+
+    def near(got, was, name, rows):
+        d = (got[0, rows, 0].double() - was[0, rows, 0].double()).abs().cpu().numpy()
+        top = np.maximum(*(np.abs(i[0, rows, 0].double().cpu().numpy()) for i in (got, was)))
+        return (d <= 2 * rel * ab[name][rows, 0] + 2 * step(BF)[0] * top + 2 * step(BF)[1]).all()
+
     if what != "do":
-        assert near(o[0, :at, 0], clean_o[0, :at, 0])
+        assert near(o, clean_o, "o", slice(0, at))
     if what == "q":
-        assert not torch.isfinite(o[0, at, 0]).any() and near(o[0, at + 1:, 0], clean_o[0, at + 1:, 0])
+        assert not torch.isfinite(o[0, at, 0]).any() and near(o, clean_o, "o", slice(at + 1, t))
         assert torch.isfinite(ST).all()
     if what in ("k", "v"):
         assert not torch.isfinite(ST[0, 0]).all()
         # dk and dv of later tokens do not depend on this token's k, v
-        assert near(r["dk"][0, at + 1:, 0], clean["dk"][0, at + 1:, 0])
-        assert near(r["dv"][0, at + 1:, 0], clean["dv"][0, at + 1:, 0])
-        assert near(r["dq"][0, :at, 0], clean["dq"][0, :at, 0])
+        assert near(r["dk"], clean["dk"], "dk", slice(at + 1, t))
+        assert near(r["dv"], clean["dv"], "dv", slice(at + 1, t))
+        assert near(r["dq"], clean["dq"], "dq", slice(0, at))
     if what in ("q", "do"):
-        assert near(r["dk"][0, at + 1:, 0], clean["dk"][0, at + 1:, 0])
-        assert near(r["dv"][0, at + 1:, 0], clean["dv"][0, at + 1:, 0])
+        assert near(r["dk"], clean["dk"], "dk", slice(at + 1, t))
+        assert near(r["dv"], clean["dv"], "dv", slice(at + 1, t))
         assert not torch.isfinite(r["dk" if what == "do" else "dv"][0, at, 0]).all()
