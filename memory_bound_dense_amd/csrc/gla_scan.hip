@@ -10,7 +10,8 @@
 namespace mbd {
 
 // ---- segments' states from their own states ----------------------------------
-// slots[s] holds segment s's own state (from zero) and becomes its start
+// slots[s] holds segment s's own state (from zero; the last segment's in the
+// order of the recurrence is not there, and not needed) and becomes its start
 // state: one thread per 4 elements walks the sequence's segments.
 struct JoinArgs {
   float* slots;
@@ -43,7 +44,7 @@ __global__ __launch_bounds__(256) void scan_join_kernel(const JoinArgs a) {
   float* slot = a.slots + head * a.nseg * size + (int64_t)d * a.dvp + e;
   const float* decay = a.decays + head * a.nseg * a.dkp + d;
 #pragma unroll 4
-  for (int s = 0; s < ns; ++s) {
+  for (int s = 0; s + 1 < ns; ++s) {
     const int64_t at = a.rev ? ns - 1 - s : s;
     f32x4* to = (f32x4*)(slot + at * size);
     const f32x4 u = *to;
@@ -51,6 +52,7 @@ __global__ __launch_bounds__(256) void scan_join_kernel(const JoinArgs a) {
     *to = x;
     x = x * f + u;
   }
+  *(f32x4*)(slot + (a.rev ? 0 : ns - 1) * size) = x;
 }
 
 }  // namespace mbd

@@ -679,12 +679,13 @@ __global__ __launch_bounds__(NW * 64, NS > 4 ? 1 : 2) void scan_out_kernel(const
       for (int m = 0; m < kMine<NW>; ++m) {
         int jt, it;
         score_tile<NW>(wave, m, jt, it);
-        bf16x8 kk[2];
+        bf16x8 kk[2], xo[2];   // xo: one of xx again, rather than a choice between registers
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
+        for (int i = 0; i < 2; ++i) {
           kk[i] = *(const bf16x8*)(ks + (i * kScanC + row_of(n, jt)) * RS + 32 * s + 8 * g);
-        if (it) pt[m] = mfma_terms<2, 2>(kk, xx[1], pt[m]);
-        else pt[m] = mfma_terms<2, 2>(kk, xx[0], pt[m]);
+          xo[i] = *(const bf16x8*)(xs + (i * kScanC + row_of(n, it)) * RS + 32 * s + 8 * g);
+        }
+        pt[m] = mfma_terms<2, 2>(kk, xo, pt[m]);
       }
       f32x4 d0 = *(const f32x4*)(dec + 32 * s + 8 * g), d1 = *(const f32x4*)(dec + 32 * s + 8 * g + 4);
 #pragma unroll
@@ -796,6 +797,8 @@ __global__ __launch_bounds__(NW * 64, NV > 4 ? 1 : 2) void scan_grad_kernel(cons
 
   Place p;
   if (!place_of(a, p)) return;
+  // the state at the far end is not a start of any segment
+  if (!GRAD && (REV ? p.seg == 0 : p.last)) return;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int n = lane & 15, g = lane >> 4;
   const int col = (p.blk * NW + wave) * 32 + 2 * n;       // the lane's channels col, col + 1
@@ -974,7 +977,8 @@ __global__ __launch_bounds__(NW * 64, NV > 4 ? 1 : 2) void scan_grad_kernel(cons
         for (int m = 0; m < kMine<NW>; ++m) {
           int jt, it;
           score_tile<NW>(wave, m, jt, it);
-          const u32x4 vv = *(const u32x4*)(vs + row_of(n, jt) * RS + 32 * s + 8 * g), wv = it ? wr[1] : wr[0];
+          const u32x4 vv = *(const u32x4*)(vs + row_of(n, jt) * RS + 32 * s + 8 * g);
+          const u32x4 wv = *(const u32x4*)(ws + row_of(n, it) * RS + 32 * s + 8 * g);
           if constexpr (DT == DT_F16)
             pt[m] = mfma(__builtin_bit_cast(f16x8, vv), __builtin_bit_cast(f16x8, wv), pt[m]);
           else
