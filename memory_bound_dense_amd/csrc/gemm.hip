@@ -169,7 +169,7 @@ bool mbd_host::gemm_set_attributes() {
   for (const auto& set : kTiles)
     for (const Tile& t : set)
       for (GemmFn f : t.fn)
-        if (f && t.lds &&
+        if (f && t.lds > 65536 &&
             hipFuncSetAttribute((const void*)f, hipFuncAttributeMaxDynamicSharedMemorySize, (int)t.lds) != hipSuccess)
           return false;
   return true;

@@ -323,14 +323,15 @@ gemv_status_t on_device(gemv_handle_t h, const char* what) {
 
 }  // namespace
 
+// Kernels with more than the default 64 KiB of dynamic LDS.
 bool mbd_host::scan_set_attributes() {
   const auto set = [](const ScanForms* forms, const size_t (&lds)[3]) {
     for (const auto& g : *forms)
       for (const auto& r : g)
         for (int t = 0; t < 3; ++t)
           for (ScanFn fn : r[t])
-            if (hipFuncSetAttribute((const void*)fn, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds[t]) !=
-                hipSuccess)
+            if (lds[t] > 65536 && hipFuncSetAttribute((const void*)fn, hipFuncAttributeMaxDynamicSharedMemorySize,
+                                                      (int)lds[t]) != hipSuccess)
               return false;
     return true;
   };
