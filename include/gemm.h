@@ -1,6 +1,6 @@
 /*
- * gemm.h -- dense product of many rows with a fused epilogue, in libgemv.so
- * next to the GEMV (same handle, same status codes, gemv.h).
+ * gemm.h -- dense product of many rows with a fused epilogue, in
+ * libmbd_operators.so, on the GEMV's handle and with its status codes (gemv.h).
  *
  * Operation, for A (m, k) -- a row per token -- and B (n, k), the weights in
  * the GEMV's layout:

@@ -1,6 +1,6 @@
 /*
  * gla_scan.h -- gated linear attention (GLA) over whole sequences, forward
- * and backward, in libgemv.so next to the one-token step (gla_decode.h; same
+ * and backward, in libmbd_operators.so; the one-token step is gla_decode.h's (same
  * handle, same status codes, gemv.h).
  *
  * Operation, for each head of each sequence (S is dk x dv, t = 1 .. tokens):

@@ -1,7 +1,7 @@
 /*
  * rmsnorm.h -- root-mean-square norm with the residual's addition, in 16 bits
- * or in 8 bits with a scale per row, in libgemv.so next to the GEMV (same
- * handle, same status codes, gemv.h).  Its 8-bit output and scales are the A
+ * or in 8 bits with a scale per row, in libmbd_operators.so, on the GEMV's
+ * handle and with its status codes (gemv.h).  Its 8-bit output and scales are the A
  * and scale_a of gemm_run (gemm.h).
  *
  * Operation, per row i of n channels:

@@ -1,5 +1,5 @@
-"""ctypes binding of the operators around the GEMV: include/gla_scan.h,
-include/gemm.h, include/rmsnorm.h.
+"""ctypes binding of libmbd_operators.so, the operators around the GEMV
+(include/operators.h, gla_scan.h, gemm.h, rmsnorm.h).
 
 Argument marshalling only, as in ``_lib``: the C functions keep their names
 and return the C status codes (pointers are addresses as ints or None); the
@@ -13,13 +13,15 @@ so calls never share scratch.  ``workspace=`` passes a tensor of the caller's
 instead.
 """
 import ctypes
+import os
 
-from . import _lib
 from ._lib import (GEMV_ERR_INVALID_ARG, GEMV_ERR_UNSUPPORTED_DTYPE, GEMV_ERR_WRONG_DEVICE, GEMV_OK,
                    Gemv, GemvError, _check_devices, _dtype_code)
 
+LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libmbd_operators.so")
+
 # every symbol these headers declare
-OPERATOR_EXPORTS = ("gla_scan_workspace_bytes", "gla_scan_forward", "gla_scan_backward",
+OPERATOR_EXPORTS = ("operators_prepare", "gla_scan_workspace_bytes", "gla_scan_forward", "gla_scan_backward",
                     "gla_scan_check_args", "gla_scan_grad_check_args", "gemm_workspace_bytes",
                     "gemm_run", "gemm_check_args", "rmsnorm_run", "rmsnorm_check_args")
 
@@ -61,10 +63,14 @@ _ready = None
 
 
 def load():
-    """libgemv.so with these operators' signatures set."""
+    """Load libmbd_operators.so (raises if it was not built)."""
     global _ready
     if _ready is None:
-        lib = _lib.load()
+        if not os.path.exists(LIB_PATH):
+            raise RuntimeError("libmbd_operators.so is not built (%s); run "
+                               "`python -m memory_bound_dense_amd.build_operators`" % LIB_PATH)
+        lib = ctypes.CDLL(LIB_PATH)
+        lib.operators_prepare.argtypes = [_vp]
         scan, grad = ctypes.POINTER(gla_scan_t), ctypes.POINTER(gla_scan_grad_t)
         lib.gla_scan_workspace_bytes.argtypes = [scan, _i32]
         lib.gla_scan_workspace_bytes.restype = _sz
@@ -87,6 +93,11 @@ def load():
 
 
 # ---- the C entry points, same names ------------------------------------------
+
+def operators_prepare(h):
+    """Set the kernels up on the handle's device now (the first call otherwise does)."""
+    return load().operators_prepare(h)
+
 
 def gla_scan_workspace_bytes(p, backward=False):
     return load().gla_scan_workspace_bytes(ctypes.byref(p), int(backward))
@@ -136,6 +147,17 @@ def rmsnorm_check_args(p, x, residual, w, sum_out, y, scales):
 
 
 # ---- torch tensors -------------------------------------------------------------
+
+def _handle(gemv):
+    """The Gemv whose handle an operator uses, with the operators set up on its device if that
+    is the current one (else the first call does it)."""
+    g = gemv if gemv is not None else Gemv()
+    if g.h is not None:
+        s = operators_prepare(g.h)
+        if s not in (GEMV_OK, GEMV_ERR_WRONG_DEVICE):
+            raise GemvError(s, "operators_prepare")
+    return g
+
 
 def _bad(what):
     return GemvError(GEMV_ERR_INVALID_ARG, what)
@@ -194,7 +216,7 @@ class GlaScan:
     sequence, and ``longest`` is the longest sequence's length (default: t)."""
 
     def __init__(self, gemv=None):
-        self.g = gemv if gemv is not None else Gemv()
+        self.g = _handle(gemv)
 
     @staticmethod
     def describe(q, v, gk, o, scale, k=None, offsets=None, longest=None):
@@ -299,7 +321,7 @@ class Gemm:
     float32.  residual may be C."""
 
     def __init__(self, gemv=None):
-        self.g = gemv if gemv is not None else Gemv()
+        self.g = _handle(gemv)
 
     def __call__(self, A, B, C, bias=None, residual=None, act="none", alpha=1.0, scale_a=None,
                  scale_b=None, workspace=None, stream=None):
@@ -334,7 +356,7 @@ class RmsNorm:
     ``scales`` (m,)."""
 
     def __init__(self, gemv=None):
-        self.g = gemv if gemv is not None else Gemv()
+        self.g = _handle(gemv)
 
     def __call__(self, x, w, y, eps=1e-6, residual=None, sum_out=None, scales=None, stream=None):
         import torch

@@ -8,22 +8,16 @@ turned off for the device code (-packed-fp32-ops).
 import os
 import subprocess
 import sys
-import tempfile
-from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libgemv.so")
-SOURCES = [os.path.join(CSRC, f) for f in (
-    "gemv.hip", "gla_scan_out_f16.hip", "gla_scan_out_bf16.hip", "gla_scan_grad_f16.hip",
-    "gla_scan_grad_bf16.hip", "gla_scan_state_f16.hip", "gla_scan_state_bf16.hip", "gemm.hip", "gla.hip",
-    "gla_scan.hip", "rmsnorm.hip")]
+SOURCES = [os.path.join(CSRC, "gemv.hip"), os.path.join(CSRC, "gla.hip")]
 DEPS = SOURCES + [os.path.join(CSRC, f) for f in ("gemv_kernel.h", "gemv_shift.h", "gemv_staged.h", "gla_kernel.h",
-                                                     "gla_scan_kernel.h", "gla_scan_table.h", "gemm_kernel.h", "handle.h",
-                                                     "operand.h")] + \
-    [os.path.join(INCLUDE, f) for f in ("gemv.h", "gla_decode.h", "gla_scan.h", "gemm.h", "rmsnorm.h")]
+                                                     "handle.h")] + \
+    [os.path.join(INCLUDE, "gemv.h"), os.path.join(INCLUDE, "gla_decode.h")]
 # measurement aid: a plain streaming read (the practical HBM read ceiling)
 PROBE_LIB = os.path.join(PKG, "libmbd_probe.so")
 PROBE_SOURCES = [os.path.join(CSRC, "stream_probe.hip")]
@@ -36,25 +30,15 @@ def hipcc():
 
 
 def _hipcc_shared(sources, out, verbose):
-    """Compile each source on its own, several at a time, and link them."""
     tmp = out + ".tmp%d" % os.getpid()
-    flags = ["--offload-arch=" + ARCH, "-O3", "-std=c++17", "-fPIC",
-             "-Wall", "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
-             # the first 16 dwords of kernel arguments arrive in SGPRs at wave launch
-             "-mllvm", "-amdgpu-kernarg-preload-count=16",
-             "-I", INCLUDE, "-I", CSRC]
-
-    def run(cmd):
-        if verbose:
-            print(" ".join(cmd), flush=True)
-        subprocess.run(cmd, check=True)
-
-    with tempfile.TemporaryDirectory() as d:
-        objects = [os.path.join(d, os.path.basename(s) + ".o") for s in sources]
-        with ThreadPoolExecutor(min(len(sources), int(os.environ.get("MAX_JOBS", "8")))) as pool:
-            list(pool.map(lambda so: run([hipcc()] + flags + ["-c", so[0], "-o", so[1]]),
-                          zip(sources, objects)))
-        run([hipcc(), "--offload-arch=" + ARCH, "-fPIC", "-shared"] + objects + ["-o", tmp])
+    cmd = [hipcc(), "--offload-arch=" + ARCH, "-O3", "-std=c++17", "-fPIC", "-shared",
+           "-Wall", "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
+           # the first 16 dwords of kernel arguments arrive in SGPRs at wave launch
+           "-mllvm", "-amdgpu-kernarg-preload-count=16",
+           "-I", INCLUDE, "-I", CSRC] + sources + ["-o", tmp]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    subprocess.run(cmd, check=True)
     os.replace(tmp, out)
 
 

@@ -1,10 +1,10 @@
-// libgemv.so, continued: the dense product of many rows with its epilogue
+// libmbd_operators.so: the dense product of many rows with its epilogue
 // (include/gemm.h) over the kernels of gemm_kernel.h.
 #include "gemm.h"
 
 #include "gemm_kernel.h"
-#include "handle.h"
 #include "operand.h"
+#include "operators.h"
 
 using mbd_host::kMagic;
 using mbd_host::Region;
@@ -192,9 +192,7 @@ extern "C" gemv_status_t gemm_run(gemv_handle_t h, const gemm_t* p, const void* 
   gemv_status_t st = check(p, A, B, C, workspace, workspace_bytes, false);
   if (st != GEMV_OK) return report(h, st, "gemm_run arguments");
   if (p->m == 0 || p->n == 0) return GEMV_OK;
-  int dev = -1;
-  if (hipGetDevice(&dev) != hipSuccess) return report(h, GEMV_ERR_HIP, "hipGetDevice");
-  if (dev != h->device) return report(h, GEMV_ERR_WRONG_DEVICE, "gemm_run");
+  if ((st = mbd_host::ready(h, "gemm_run")) != GEMV_OK) return st;
   const GemmPlan g = gemm_plan(p, whole_rows(p, A, B));
   const int64_t e = in_bytes(p->in_type);
   mbd::GemmArgs a = {};

@@ -763,10 +763,6 @@ extern "C" gemv_status_t gemv_create(gemv_handle_t* out) {
       }
     }
   }
-  if (!mbd_host::scan_set_attributes() || !mbd_host::gemm_set_attributes()) {
-    free(h);
-    return report(nullptr, GEMV_ERR_HIP, "hipFuncSetAttribute(max dynamic LDS)");
-  }
   h->magic = kMagic;
   h->device = dev;
   h->num_cus = prop.multiProcessorCount;

@@ -1,11 +1,11 @@
-// libgemv.so, continued: gated linear attention over whole sequences
+// libmbd_operators.so: gated linear attention over whole sequences
 // (include/gla_scan.h) over the kernels of gla_scan_kernel.h.
 #include "gla_scan.h"
 
 #include "gla_scan_kernel.h"
 #include "gla_scan_table.h"
-#include "handle.h"
 #include "operand.h"
+#include "operators.h"
 
 namespace mbd {
 
@@ -314,16 +314,8 @@ hipError_t launch_join(const gla_scan_t* p, const ScanPlan& s, float* slots, con
 // A grid's work-items along x (a 32-bit field of the dispatch) are kept at most 2^31.
 bool grid_fits(int64_t grid, int threads) { return grid <= ((int64_t)1 << 31) / threads; }
 
-gemv_status_t on_device(gemv_handle_t h, const char* what) {
-  int dev = -1;
-  if (hipGetDevice(&dev) != hipSuccess) return report(h, GEMV_ERR_HIP, "hipGetDevice");
-  if (dev != h->device) return report(h, GEMV_ERR_WRONG_DEVICE, what);
-  return GEMV_OK;
-}
-
 }  // namespace
 
-// Kernels with more than the default 64 KiB of dynamic LDS.
 bool mbd_host::scan_set_attributes() {
   const auto set = [](const ScanForms* forms, const size_t (&lds)[3]) {
     for (const auto& g : *forms)
@@ -371,7 +363,7 @@ extern "C" gemv_status_t gla_scan_forward(gemv_handle_t h, const gla_scan_t* p, 
   gemv_status_t st = check_forward(p, q, k, v, gk, S0, ST, o, workspace, workspace_bytes, &idle);
   if (st != GEMV_OK) return report(h, st, "gla_scan_forward arguments");
   if (idle || (p->tokens == 0 && !ST)) return GEMV_OK;
-  if ((st = on_device(h, "gla_scan_forward")) != GEMV_OK) return st;
+  if ((st = mbd_host::ready(h, "gla_scan_forward")) != GEMV_OK) return st;
   const ScanPlan s = scan_plan(p, false);
   const int64_t bh = s.heads;
   mbd::ScanArgs a = common(p, s);
@@ -422,7 +414,7 @@ extern "C" gemv_status_t gla_scan_backward(gemv_handle_t h, const gla_scan_t* p,
                                     workspace_bytes, &idle);
   if (st != GEMV_OK) return report(h, st, "gla_scan_backward arguments");
   if (idle || (p->tokens == 0 && !dS0)) return GEMV_OK;
-  if ((st = on_device(h, "gla_scan_backward")) != GEMV_OK) return st;
+  if ((st = mbd_host::ready(h, "gla_scan_backward")) != GEMV_OK) return st;
   const ScanPlan s = scan_plan(p, true);
   char* w = (char*)workspace;
   const mbd::ScanTensor tq = tensor(p, q, p->q, p->dk), tk = tensor(p, k, p->k, p->dk),

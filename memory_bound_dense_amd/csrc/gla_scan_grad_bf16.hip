@@ -1,4 +1,4 @@
-// libgemv.so, continued: the bf16 forms of scan_grad_kernel.
+// libmbd_operators.so: the bf16 forms of scan_grad_kernel.
 #include "gla_scan_table.h"
 
 namespace mbd {

@@ -1,4 +1,4 @@
-// libgemv.so, continued: the f16 forms of scan_grad_kernel.
+// libmbd_operators.so: the f16 forms of scan_grad_kernel.
 #include "gla_scan_table.h"
 
 namespace mbd {

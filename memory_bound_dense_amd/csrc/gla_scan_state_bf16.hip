@@ -1,4 +1,4 @@
-// libgemv.so, continued: the bf16 forms of scan_grad_kernel that leave a segment's own state.
+// libmbd_operators.so: the bf16 forms of scan_grad_kernel that leave a segment's own state.
 #include "gla_scan_table.h"
 
 namespace mbd {

@@ -19,10 +19,6 @@ constexpr uint32_t kMagic = 0x47454d56u;   // "GEMV"
 constexpr uint32_t kDead = 0xdeadbeefu;
 constexpr int kMaxVariants = 96;
 
-// Kernel attributes of the other operators on the current device, set by gemv_create.
-bool scan_set_attributes();
-bool gemm_set_attributes();
-
 }  // namespace mbd_host
 
 struct gemv_handle_s {

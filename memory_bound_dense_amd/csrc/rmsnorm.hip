@@ -1,4 +1,4 @@
-// libgemv.so, continued: root-mean-square norm with residual addition and
+// libmbd_operators.so: root-mean-square norm with residual addition and
 // 16-bit or scaled 8-bit output (include/rmsnorm.h).
 //
 // Bound by HBM: x and residual are read once, s and y written once.  A
@@ -9,8 +9,8 @@
 #include "rmsnorm.h"
 
 #include "gemv_kernel.h"
-#include "handle.h"
 #include "operand.h"
+#include "operators.h"
 
 using mbd_host::kMagic;
 using mbd_host::Region;
@@ -262,9 +262,7 @@ extern "C" gemv_status_t rmsnorm_run(gemv_handle_t h, const rmsnorm_t* p, const 
   gemv_status_t st = rmsnorm_check_args(p, x, residual, w, sum_out, y, scales);
   if (st != GEMV_OK) return report(h, st, "rmsnorm_run arguments");
   if (p->m == 0 || p->n == 0) return GEMV_OK;
-  int dev = -1;
-  if (hipGetDevice(&dev) != hipSuccess) return report(h, GEMV_ERR_HIP, "hipGetDevice");
-  if (dev != h->device) return report(h, GEMV_ERR_WRONG_DEVICE, "rmsnorm_run");
+  if ((st = mbd_host::ready(h, "rmsnorm_run")) != GEMV_OK) return st;
   mbd::NormArgs a = {(const uint16_t*)x, (const uint16_t*)residual, (const uint16_t*)w, (uint16_t*)sum_out, y, scales,
                      p->ldx, p->ldres, p->ldsum, p->ldy, (int32_t)p->n, p->eps};
   const auto whole = [&](const void* q, int64_t ld) { return !q || (((uintptr_t)q & 15u) == 0 && ld % 8 == 0); };

@@ -4,6 +4,8 @@ formulas of tests/scan_ref.py against differences."""
 import ctypes
 import os
 import re
+import shutil
+import subprocess
 
 import numpy as np
 import pytest
@@ -15,7 +17,7 @@ from memory_bound_dense_amd import _lib
 from memory_bound_dense_amd import _operators as ops
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
-HEADERS = ["gla_scan.h", "gemm.h", "rmsnorm.h"]
+HEADERS = ["operators.h", "gla_scan.h", "gemm.h", "rmsnorm.h"]
 OK, INVALID, DTYPE, MISALIGNED, ALIASING, TOO_LARGE = (
     _lib.GEMV_OK, _lib.GEMV_ERR_INVALID_ARG, _lib.GEMV_ERR_UNSUPPORTED_DTYPE, _lib.GEMV_ERR_MISALIGNED,
     _lib.GEMV_ERR_ALIASING, _lib.GEMV_ERR_TOO_LARGE)
@@ -30,15 +32,36 @@ def test_headers_and_library_agree_with_the_binding():
     names = set()
     for h in HEADERS:
         text = re.sub(r"/\*.*?\*/", "", open(os.path.join(ROOT, "include", h)).read(), flags=re.S)
-        names |= set(re.findall(r"^\s*(?:const\s+)?\w+\**\s+\**((?:gla_scan|gemm|rmsnorm)_\w+)\s*\(", text,
+        names |= set(re.findall(r"^\s*(?:const\s+)?\w+\**\s+\**((?:operators|gla_scan|gemm|rmsnorm)_\w+)\s*\(", text,
                                 flags=re.M))
     assert sorted(names) == sorted(ops.OPERATOR_EXPORTS)
-    lib = ctypes.CDLL(_lib.LIB_PATH)
+    lib = ctypes.CDLL(ops.LIB_PATH)
     for n in names:
         assert hasattr(lib, n), n
 
 
+def test_headers_compile_as_c(tmp_path):
+    """The headers as C99, and every entry point linked from the library by a C program."""
+    cc = shutil.which("gcc") or shutil.which("cc")
+    if cc is None:
+        pytest.skip("no C compiler")
+    src, exe = tmp_path / "use.c", str(tmp_path / "use")
+    src.write_text("#include <stdio.h>\n#include \"operators.h\"\nint main(void) {\n  void* fns[] = {%s};\n"
+                   "  gemm_t g = {0};\n  int n = 0;\n"
+                   "  for (unsigned i = 0; i < sizeof(fns) / sizeof(fns[0]); ++i) n += fns[i] != NULL;\n"
+                   "  printf(\"%%d %%d\", n, (int)gemm_check_args(&g, NULL, NULL, NULL, NULL, 0));\n  return 0;\n}\n"
+                   % ", ".join("(void*)&" + n for n in ops.OPERATOR_EXPORTS))
+    lib = os.path.dirname(ops.LIB_PATH)
+    built = subprocess.run([cc, "-std=c99", "-Wall", "-Werror", "-isystem", "/opt/rocm/include", "-D__HIP_PLATFORM_AMD__",
+                            "-I", os.path.join(ROOT, "include"), str(src), "-L", lib, "-lmbd_operators",
+                            "-Wl,-rpath," + lib, "-o", exe], capture_output=True, text=True)
+    assert built.returncode == 0, built.stderr
+    ran = subprocess.run([exe], capture_output=True, text=True, timeout=120)
+    assert ran.stdout == "%d 0" % len(ops.OPERATOR_EXPORTS), ran.stderr
+
+
 def test_null_handles():
+    assert ops.operators_prepare(None) == _lib.GEMV_ERR_NULL_HANDLE
     p = scan()
     assert ops.gla_scan_forward(None, p, *[at(i) for i in range(7)]) == _lib.GEMV_ERR_NULL_HANDLE
     assert ops.gla_scan_backward(None, p, grads(p), *[at(i) for i in range(12)]) == _lib.GEMV_ERR_NULL_HANDLE
