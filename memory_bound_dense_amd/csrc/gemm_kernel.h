@@ -524,7 +524,8 @@ __device__ __forceinline__ void load_to_lds(__amdgpu_buffer_rsrc_t r, uint8_t* t
   __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)to, 16, off, 0, 0, 0);
 }
 
-// Every wave's loads but its last N have landed, for every wave of the workgroup.
+// Every wave's loads into LDS but its last N, and all its LDS accesses, are done
+// for every wave of the workgroup.
 template <int N>
 __device__ __forceinline__ void step_barrier() {
   asm volatile("" ::: "memory");
@@ -638,7 +639,7 @@ __global__ __launch_bounds__(WN * WM * WK * 64, 2) void gemm_direct_kernel(const
 #pragma unroll
         for (int t = 0; t < TM; ++t) a[t] = *(const u32x4*)(ab + t * 16 * 128 + c0);
         u32x4 b = *(const u32x4*)(bb + c0);
-  #pragma unroll
+#pragma unroll
         for (int n = 0; n < TN; ++n) {
           u32x4 next = b;
           if (n + 1 < TN) next = *(const u32x4*)(bb + (n + 1) * 16 * 128 + c0);
@@ -646,20 +647,20 @@ __global__ __launch_bounds__(WN * WM * WK * 64, 2) void gemm_direct_kernel(const
           for (int t = 0; t < TM; ++t) c[n][t] = half_mfma<IN>(b, a[t], c[n][t]);
           b = next;
         }
-        }
+      }
     }
   };
   if constexpr (ST == 2) {
     if (s0 < s1) issue(buf0, s0);
-    __syncthreads();
+    step_barrier<0>();
     for (int s = s0; s < s1; s += 2) {
       if (s + 1 < s1) issue(buf1, s + 1);
       use(buf0);
-      __syncthreads();
+      step_barrier<0>();
       if (s + 1 < s1) {
         if (s + 2 < s1) issue(buf0, s + 2);
         use(buf1);
-        __syncthreads();
+        step_barrier<0>();
       }
     }
   } else {
@@ -670,11 +671,11 @@ __global__ __launch_bounds__(WN * WM * WK * 64, 2) void gemm_direct_kernel(const
       if (s + 2 < s1) issue(far, s + 2);
       use(now);
       if (s + 2 < full && s + 2 < s1) step_barrier<LPW>();
-      else __syncthreads();
+      else step_barrier<0>();
     };
     if (s0 < s1) issue(buf0, s0);
     if (s0 + 1 < s1) issue(buf1, s0 + 1);
-    __syncthreads();
+    step_barrier<0>();
     for (int s = s0; s < s1; s += 3) {
       step(buf2, buf0, s);
       if (s + 1 < s1) step(buf0, buf1, s + 1);

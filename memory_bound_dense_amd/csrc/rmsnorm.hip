@@ -80,14 +80,17 @@ __device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d) {
   return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c, d, w, true);
 }
 
+// A row's factors.  inv = 448 / max |u| leaves fp32's range below 2^-119; rows of
+// so small values are raised by `up` first.
 struct RowScale {
-  float r, scale, inv;
+  float r, scale, up, inv;
 };
 __device__ __forceinline__ RowScale row_scale(const NormArgs& p, float ss, float mx) {
   RowScale s;
   s.r = 1.0f / sqrtf(ss / (float)p.n + p.eps);
   s.scale = s.r * mx / 448.0f;
-  s.inv = mx > 0.0f ? 448.0f / mx : 0.0f;
+  s.up = mx < 0x1p-100f ? 0x1p100f : 1.0f;
+  s.inv = mx > 0.0f ? 448.0f / (mx * s.up) : 0.0f;
   return s;
 }
 
@@ -155,9 +158,13 @@ __global__ __launch_bounds__(T) void norm_kernel(const NormArgs p) {
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
       const uint32_t a = s[i][c], b = w[i][c];
-      const float f = E4M3 ? 1.0f : k.r;
-      u[2 * c] = norm_lo<DT>(a) * f * norm_lo<DT>(b);
-      u[2 * c + 1] = norm_hi<DT>(a) * f * norm_hi<DT>(b);
+      if (E4M3) {
+        u[2 * c] = norm_lo<DT>(a) * norm_lo<DT>(b) * k.up;
+        u[2 * c + 1] = norm_hi<DT>(a) * norm_hi<DT>(b) * k.up;
+      } else {
+        u[2 * c] = norm_lo<DT>(a) * k.r * norm_lo<DT>(b);
+        u[2 * c + 1] = norm_hi<DT>(a) * k.r * norm_hi<DT>(b);
+      }
     }
     if (E4M3) {
       u32x2 o;
@@ -198,7 +205,7 @@ __global__ __launch_bounds__(256) void norm_any_kernel(const NormArgs p) {
     uint16_t b = sr ? sr[j] : xr[j];
     if (rr && !sr) b = to_bits<DT>(widen<DT>(b) + widen<DT>(rr[j]));
     const float s = widen<DT>(b), w = widen<DT>(p.w[j]);
-    if (E4M3) ((uint8_t*)p.y)[row * p.ldy + j] = (uint8_t)codes4(s * w * k.inv, 0.0f, 0.0f, 0.0f);
+    if (E4M3) ((uint8_t*)p.y)[row * p.ldy + j] = (uint8_t)codes4(s * w * k.up * k.inv, 0.0f, 0.0f, 0.0f);
     else ((uint16_t*)p.y)[row * p.ldy + j] = to_bits<DT>(s * k.r * w);
   }
 }

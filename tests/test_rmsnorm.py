@@ -129,6 +129,19 @@ def test_zero_and_special_rows(norm, n):
     check8(y[3:], sc[3:], z, n)
 
 
+@pytest.mark.parametrize("n", [64, 333])
+def test_tiny_rows(norm, n):
+    """s w near 2^-124: 448 over the row's largest is beyond float32."""
+    gen = torch.Generator().manual_seed(n)
+    x, w = torch.randn(3, n, generator=gen).mul(2.0 ** -60).to(BF), torch.full((n,), 2.0 ** -64, dtype=BF)
+    x[:, ::5] = 0
+    _, z = want(x, None, w, 1e-6)
+    y, sc = torch.empty(3, n, device="cuda").to(E4), torch.empty(3, device="cuda")
+    norm(x.cuda(), w.cuda(), y, scales=sc)
+    torch.cuda.synchronize()
+    check8(y, sc, z, n)
+
+
 def test_empty(norm):
     w = torch.empty(0, dtype=BF, device="cuda")
     norm(torch.empty(3, 0, dtype=BF, device="cuda"), w, torch.empty(3, 0, dtype=BF, device="cuda"))
