@@ -13,7 +13,7 @@ namespace mbd {
 // slots[s] holds segment s's own state (from zero; the last segment's in the
 // order of the recurrence is not there, and not needed) and becomes its start
 // state: one thread per 4 elements walks the sequence's segments.
-struct JoinArgs {
+struct Join {
   float* slots;
   const float* decays;
   const float* S0;          // user layout, or null
@@ -21,7 +21,11 @@ struct JoinArgs {
   int64_t total, t;
   int32_t H, dk, dv, dkp, dvp, nseg, L, rev;
 };
-__global__ __launch_bounds__(256) void scan_join_kernel(const JoinArgs a) {
+struct JoinArgs {
+  Join side[2];             // by grid y: a backward pass has two
+};
+__global__ __launch_bounds__(256) void scan_join_kernel(const JoinArgs both) {
+  const Join& a = both.side[blockIdx.y];
   const int per = a.dkp * (a.dvp / 4), nx = (per + 255) / 256;
   const int64_t head = blockIdx.x / nx;            // seq * H + h
   const int seq = (int)(head / a.H);
@@ -50,7 +54,9 @@ __global__ __launch_bounds__(256) void scan_join_kernel(const JoinArgs a) {
     const f32x4 u = *to;
     const float f = decay[at * a.dkp];
     *to = x;
-    x = x * f + u;
+    // a state of zeros stays one, also where the segment's decay is beyond float32
+#pragma unroll
+    for (int r = 0; r < 4; ++r) x[r] = x[r] == 0.0f && f > 3e38f ? u[r] : __builtin_fmaf(x[r], f, u[r]);
   }
   *(f32x4*)(slot + (a.rev ? 0 : ns - 1) * size) = x;
 }
@@ -259,11 +265,12 @@ using mbd::ScanFn;
 using mbd::ScanForms;
 const ScanForms* const kScanOut[2] = {&mbd::kScanOutF16, &mbd::kScanOutBf16};
 const ScanForms* const kScanGrad[2] = {&mbd::kScanGradF16, &mbd::kScanGradBf16};
-const ScanForms* const kScanState[2] = {&mbd::kScanStateF16, &mbd::kScanStateBf16};
+const mbd::StateForms* const kScanState[2] = {&mbd::kScanStateF16, &mbd::kScanStateBf16};
 ScanFn scan_form(const ScanForms* const (&forms)[2], const gla_scan_t* p, int rev, int tier, bool four) {
   return (*forms[p->dtype])[p->gate_f32][rev][tier][four];
 }
 const size_t kOutLds[3] = {mbd::scan_out_lds<2>(), mbd::scan_out_lds<4>(), mbd::scan_out_lds<8>()};
+const size_t kStateLds[3] = {mbd::scan_state_lds<2>(), mbd::scan_state_lds<4>(), mbd::scan_state_lds<8>()};
 const size_t kGradLds[3] = {mbd::scan_grad_lds<2>(), mbd::scan_grad_lds<4>(), mbd::scan_grad_lds<8>()};
 
 // 64, 128 or 256 channels, by index.
@@ -301,14 +308,25 @@ hipError_t launch(ScanFn fn, int64_t grid, int waves, size_t lds, const mbd::Sca
   return hipLaunchKernel((const void*)fn, dim3((unsigned)grid), dim3((unsigned)waves * 64u), args, lds, stream);
 }
 
-hipError_t launch_join(const gla_scan_t* p, const ScanPlan& s, float* slots, const float* decays, const float* S0,
-                       int rev, hipStream_t stream) {
-  mbd::JoinArgs j = {slots, decays, S0, p->offsets, p->rows, p->tokens, (int32_t)p->heads, (int32_t)p->dk,
-                     (int32_t)p->dv, s.dkp, s.dvp, s.nseg, s.L, rev};
+// Own states of the segments, over `dv` columns; `sides` 2: of both recurrences
+// (15 heads of 64 x 96, 1001 tokens: 19 us one after the other).
+hipError_t launch_state(const gla_scan_t* p, int64_t grid, int waves, int64_t dv, const mbd::StateArgs& a, int sides,
+                        hipStream_t stream) {
+  const int t = tier(dv);
+  void* args[] = {(void*)&a};
+  return hipLaunchKernel((const void*)(*kScanState[p->dtype])[p->gate_f32][t][waves == 4],
+                         dim3((unsigned)grid, (unsigned)sides), dim3((unsigned)waves * 64u), args, kStateLds[t], stream);
+}
+
+mbd::Join join_of(const gla_scan_t* p, const ScanPlan& s, float* slots, const float* decays, const float* S0, int rev) {
+  return mbd::Join{slots, decays, S0, p->offsets, p->rows, p->tokens, (int32_t)p->heads, (int32_t)p->dk,
+                   (int32_t)p->dv, s.dkp, s.dvp, s.nseg, s.L, rev};
+}
+hipError_t launch_join(const ScanPlan& s, const mbd::JoinArgs& j, int sides, hipStream_t stream) {
   void* args[] = {(void*)&j};
   const int64_t nx = ((int64_t)s.dkp * (s.dvp / 4) + 255) / 256;
-  return hipLaunchKernel((const void*)&mbd::scan_join_kernel, dim3((unsigned)(nx * s.heads)), dim3(256), args, 0,
-                         stream);
+  return hipLaunchKernel((const void*)&mbd::scan_join_kernel, dim3((unsigned)(nx * s.heads), (unsigned)sides),
+                         dim3(256), args, 0, stream);
 }
 
 // A grid's work-items along x (a 32-bit field of the dispatch) are kept at most 2^31.
@@ -317,18 +335,18 @@ bool grid_fits(int64_t grid, int threads) { return grid <= ((int64_t)1 << 31) / 
 }  // namespace
 
 bool mbd_host::scan_set_attributes() {
-  const auto set = [](const ScanForms* forms, const size_t (&lds)[3]) {
-    for (const auto& g : *forms)
-      for (const auto& r : g)
-        for (int t = 0; t < 3; ++t)
-          for (ScanFn fn : r[t])
-            if (lds[t] > 65536 && hipFuncSetAttribute((const void*)fn, hipFuncAttributeMaxDynamicSharedMemorySize,
-                                                      (int)lds[t]) != hipSuccess)
-              return false;
-    return true;
+  const auto set = [](const void* fn, size_t lds) {
+    return lds <= 65536 || hipFuncSetAttribute(fn, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds) == hipSuccess;
   };
+  static_assert(mbd::scan_state_lds<8>() <= 65536, "");
   for (int d = 0; d < 2; ++d)
-    if (!set(kScanOut[d], kOutLds) || !set(kScanGrad[d], kGradLds) || !set(kScanState[d], kGradLds)) return false;
+    for (int g = 0; g < 2; ++g)
+      for (int r = 0; r < 2; ++r)
+        for (int t = 0; t < 3; ++t)
+          for (int w = 0; w < 2; ++w)
+            if (!set((const void*)(*kScanOut[d])[g][r][t][w], kOutLds[t]) ||
+                !set((const void*)(*kScanGrad[d])[g][r][t][w], kGradLds[t]))
+              return false;
   return true;
 }
 
@@ -386,7 +404,8 @@ extern "C" gemv_status_t gla_scan_forward(gemv_handle_t h, const gla_scan_t* p, 
     a.slots = (float*)(w + s.slots);
     a.decays = (float*)(w + s.decays);
     // a segment's own state: columns in blocks of at most 256, channels in blocks of a workgroup's
-    mbd::ScanArgs b = a;
+    mbd::StateArgs sides = {a, {}};
+    mbd::ScanArgs& b = sides.fwd;
     const int kw = waves_of(p->dk);
     b.nblk = (int32_t)((p->dk + 32 * kw - 1) / (32 * kw));
     for (int64_t c0 = 0; c0 < p->dv && e == hipSuccess; c0 += 256) {
@@ -394,9 +413,9 @@ extern "C" gemv_status_t gla_scan_forward(gemv_handle_t h, const gla_scan_t* p, 
       b.V.p = (const char*)a.V.p + c0 * 2;
       b.dv = (int32_t)c;
       b.ecol = (int32_t)c0;
-      e = launch(scan_form(kScanState, p, 0, tier(c), kw == 4), bh * s.nseg * b.nblk, kw, kGradLds[tier(c)], b, stream);
+      e = launch_state(p, bh * s.nseg * b.nblk, kw, c, sides, 1, stream);
     }
-    if (e == hipSuccess) e = launch_join(p, s, a.slots, a.decays, S0, 0, stream);
+    if (e == hipSuccess) e = launch_join(s, {{join_of(p, s, a.slots, a.decays, S0, 0), {}}}, 1, stream);
   }
   const int ow = waves_of(a.cols);
   if (e == hipSuccess) e = launch(scan_form(kScanOut, p, 0, tier(p->dk), ow == 4), grid, ow, kOutLds[tier(p->dk)], a, stream);
@@ -462,10 +481,9 @@ extern "C" gemv_status_t gla_scan_backward(gemv_handle_t h, const gla_scan_t* p,
     r.slots = o.slots = (float*)(w + s.slots2);
     r.decays = o.decays = (float*)(w + s.decays2);
     f.others = r.slots;
-    e = launch(scan_form(kScanState, p, 0, vt, kw == 4), gk_grid, kw, kGradLds[vt], f, stream);
-    if (e == hipSuccess) e = launch(scan_form(kScanState, p, 1, vt, kw == 4), gk_grid, kw, kGradLds[vt], r, stream);
-    if (e == hipSuccess) e = launch_join(p, s, f.slots, f.decays, S0, 0, stream);
-    if (e == hipSuccess) e = launch_join(p, s, r.slots, r.decays, dST, 1, stream);
+    e = launch_state(p, gk_grid, kw, p->dv, {f, r}, 2, stream);
+    if (e == hipSuccess)
+      e = launch_join(s, {{join_of(p, s, f.slots, f.decays, S0, 0), join_of(p, s, r.slots, r.decays, dST, 1)}}, 2, stream);
   }
   if (e == hipSuccess) e = launch(scan_form(kScanGrad, p, 0, vt, kw == 4), gk_grid, kw, kGradLds[vt], f, stream);
   if (e == hipSuccess) e = launch(scan_form(kScanGrad, p, 1, vt, kw == 4), gk_grid, kw, kGradLds[vt], r, stream);

@@ -3,7 +3,7 @@
 
 namespace mbd {
 
-#define FORM(G32, N, REV) {&scan_grad_kernel<DT_BF16, G32, N, 2, REV, true>, &scan_grad_kernel<DT_BF16, G32, N, 4, REV, true>}
+#define FORM(G32, N, REV) {&scan_grad_kernel<DT_BF16, G32, N, 2, REV>, &scan_grad_kernel<DT_BF16, G32, N, 4, REV>}
 #define FORMS(G32, REV) {FORM(G32, 2, REV), FORM(G32, 4, REV), FORM(G32, 8, REV)}
 extern const ScanForms kScanGradBf16 = {{FORMS(false, false), FORMS(false, true)}, {FORMS(true, false), FORMS(true, true)}};
 

@@ -769,7 +769,7 @@ __global__ __launch_bounds__(NW * 64, NS > 4 ? 1 : 2) void scan_out_kernel(const
   }
 }
 
-// ---- out_i = S W_i, and a segment's own state -------------------------------
+// ---- out_i = S W_i ------------------------------------------------------------
 // A wave owns 32 channels (columns of the transposed state, 64 VGPRs at DV
 // 128) and their part of the output; K e^{r-G} of its channels never leaves
 // its registers.  V and W go through LDS, row-major for the products over DV
@@ -780,7 +780,7 @@ constexpr size_t scan_grad_lds() {
   return (size_t)2 * kScanC * (NV * 32 + kPadRow) * 2 + (size_t)NV * 32 * kTokRow * 2 + 6144 + 64;
 }
 
-template <int DT, bool G32, int NV, int NW, bool REV, bool GRAD>
+template <int DT, bool G32, int NV, int NW, bool REV>
 __global__ __launch_bounds__(NW * 64, NV > 4 ? 1 : 2) void scan_grad_kernel(const ScanArgs a) {
   constexpr int DVP = NV * 32, RS = DVP + kPadRow;
   constexpr int gb = G32 ? 4 : 2;
@@ -797,8 +797,6 @@ __global__ __launch_bounds__(NW * 64, NV > 4 ? 1 : 2) void scan_grad_kernel(cons
 
   Place p;
   if (!place_of(a, p)) return;
-  // the state at the far end is not a start of any segment
-  if (!GRAD && (REV ? p.seg == 0 : p.last)) return;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int n = lane & 15, g = lane >> 4;
   const int col = (p.blk * NW + wave) * 32 + 2 * n;       // the lane's channels col, col + 1
@@ -806,15 +804,15 @@ __global__ __launch_bounds__(NW * 64, NV > 4 ? 1 : 2) void scan_grad_kernel(cons
   float* slot = a.slots ? a.slots + p.slot * (int64_t)a.dkp * a.dvp : nullptr;
 
   f32x4 S[NV][2][2];   // rows: DV, columns: the lane's channels
+  auto load_state = [&] {
 #pragma unroll
-  for (int s = 0; s < NV; ++s)
+    for (int s = 0; s < NV; ++s)
 #pragma unroll
-    for (int tl = 0; tl < 2; ++tl)
+      for (int tl = 0; tl < 2; ++tl)
 #pragma unroll
-      for (int nt = 0; nt < 2; ++nt) {
-        const int e = 32 * s + 8 * g + 4 * tl;
-        f32x4 x = {};
-        if (GRAD) {
+        for (int nt = 0; nt < 2; ++nt) {
+          const int e = 32 * s + 8 * g + 4 * tl;
+          f32x4 x = {};
           if (slot) {
             if (col + nt < a.dkp && e < a.dvp) x = *(const f32x4*)(slot + (int64_t)(col + nt) * a.dvp + e);
           } else if (a.S0 && col + nt < a.dk) {
@@ -822,39 +820,33 @@ __global__ __launch_bounds__(NW * 64, NV > 4 ? 1 : 2) void scan_grad_kernel(cons
             for (int r = 0; r < 4; ++r)
               if (e + r < a.dv) x[r] = a.S0[(head * a.dk + col + nt) * a.dv + e + r];
           }
+          S[s][tl][nt] = x;
         }
-        S[s][tl][nt] = x;
-      }
+  };
+  // Behind the first chunk, which is needed before it (forward), or before it (reversed): 15 heads
+  // of 64 x 96, 1001 tokens 28.4 us for 30.8, and 32.7 for 36.2.
+  if (REV) load_state();
 
   const char *kb = base_of<REV>(a.K, p, 2), *vb = base_of<REV>(a.V, p, 2), *gbp = base_of<REV>(a.G, p, gb);
-  const char *xb = nullptr, *wb = nullptr, *ob = nullptr, *dgb = nullptr;
-  float* qdq = nullptr;
-  float carry[2] = {0.0f, 0.0f}, all_decay[2] = {1.0f, 1.0f};
-  if (GRAD) {
-    xb = base_of<REV>(a.X, p, 2);
-    wb = base_of<REV>(a.W, p, 2);
-    ob = base_of<REV>(a.O, p, 2);
-    if (REV) dgb = base_of<REV>(a.DG, p, gb);
-    // rows of all sequences in one run: (b t + token, h, dkp)
-    qdq = a.qdq + ((p.b * a.t + p.row0) * a.H + p.h) * a.dkp;
-    if (REV) {
+  const char *xb = base_of<REV>(a.X, p, 2), *wb = base_of<REV>(a.W, p, 2), *ob = base_of<REV>(a.O, p, 2), *dgb = nullptr;
+  // rows of all sequences in one run: (b t + token, h, dkp)
+  float* qdq = a.qdq + ((p.b * a.t + p.row0) * a.H + p.h) * a.dkp;
+  float carry[2] = {0.0f, 0.0f};
+  if (REV) {
+    dgb = base_of<REV>(a.DG, p, gb);
 #pragma unroll
-      for (int nt = 0; nt < 2; ++nt)
-        if (col + nt < a.dkp) carry[nt] = a.ends[p.slot * a.dkp + col + nt];
-    }
+    for (int nt = 0; nt < 2; ++nt)
+      if (col + nt < a.dkp) carry[nt] = a.ends[p.slot * a.dkp + col + nt];
   }
   const Lane kl = lane_of<REV>(a.K, g, col, a.dk, 2), gl = lane_of<REV>(a.G, g, col, a.dk, gb);
-  Lane xl = kl, ol = kl, dl = kl, wl[SL], vl[SL];
-  if (GRAD) {
-    xl = lane_of<REV>(a.X, g, col, a.dk, 2);
-    ol = lane_of<REV>(a.O, g, col, a.dk, 2);
-    if (REV) dl = lane_of<REV>(a.DG, g, col, a.dk, gb);
-  }
+  const Lane xl = lane_of<REV>(a.X, g, col, a.dk, 2), ol = lane_of<REV>(a.O, g, col, a.dk, 2);
+  Lane dl = kl, wl[SL], vl[SL];
+  if (REV) dl = lane_of<REV>(a.DG, g, col, a.dk, gb);
 #pragma unroll
   for (int i = 0; i < SL; ++i) {
     const int e0 = 32 * (wave + i * NW) + 2 * n;
     vl[i] = lane_of<REV>(a.V, g, e0, a.dv, 2);
-    if (GRAD) wl[i] = lane_of<REV>(a.W, g, e0, a.dv, 2);
+    wl[i] = lane_of<REV>(a.W, g, e0, a.dv, 2);
   }
 
   const int nch = (int)((p.hi - p.lo + kScanC - 1) / kScanC);
@@ -865,12 +857,10 @@ __global__ __launch_bounds__(NW * 64, NV > 4 ? 1 : 2) void scan_grad_kernel(cons
     const auto vr = chunk_rsrc(a.V, vb, nv, a.dv, 2);
 #pragma unroll
     for (int i = 0; i < SL; ++i) load16<REV>(vr, vl[i], a.V.vec, vw[i]);
-    if (GRAD) {
-      const auto wr = chunk_rsrc(a.W, wb, nv, a.dv, 2);
+    const auto wr = chunk_rsrc(a.W, wb, nv, a.dv, 2);
 #pragma unroll
-      for (int i = 0; i < SL; ++i) load16<REV>(wr, wl[i], a.W.vec, ww[i]);
-      walk<REV>(a.W, wb, 2);
-    }
+    for (int i = 0; i < SL; ++i) load16<REV>(wr, wl[i], a.W.vec, ww[i]);
+    walk<REV>(a.W, wb, 2);
     load_gates<REV, G32>(chunk_rsrc(a.G, gbp, nv, a.dk, gb), gl, a.G.vec, gw);
     load16<REV>(chunk_rsrc(a.K, kb, nv, a.dk, 2), kl, a.K.vec, kw);
     walk<REV>(a.V, vb, 2);
@@ -878,6 +868,7 @@ __global__ __launch_bounds__(NW * 64, NV > 4 ? 1 : 2) void scan_grad_kernel(cons
     walk<REV>(a.K, kb, 2);
   };
   if (nch > 0) fetch(0);
+  if (!REV) load_state();
   float left[2] = {1.0f, 1.0f};   // a step's second half e^{end-r}, done with the next step's first
   Step st = {0, 32};
   for (int c = 0; c < nch;) {
@@ -897,15 +888,13 @@ __global__ __launch_bounds__(NW * 64, NV > 4 ? 1 : 2) void scan_grad_kernel(cons
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         raw = pair_max(raw, v[j]);
-        if (GRAD) *(uint32_t*)(vs + (8 * g + j) * RS + e0) = v[j];
+        *(uint32_t*)(vs + (8 * g + j) * RS + e0) = v[j];
       }
-      if (GRAD) {
-        take(st, g, ww[i], v);
+      take(st, g, ww[i], v);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          raw = pair_max(raw, v[j]);
-          *(uint32_t*)(ws + (8 * g + j) * RS + e0) = v[j];
-        }
+      for (int j = 0; j < 8; ++j) {
+        raw = pair_max(raw, v[j]);
+        *(uint32_t*)(ws + (8 * g + j) * RS + e0) = v[j];
       }
       hard |= pair_wild<DT>(raw);
     }
@@ -943,17 +932,13 @@ __global__ __launch_bounds__(NW * 64, NV > 4 ? 1 : 2) void scan_grad_kernel(cons
       continue;
     }
 
-    if (!GRAD) {
-      all_decay[0] *= q.a[0] * q.b[0];
-      all_decay[1] *= q.a[1] * q.b[1];
-    }
 #pragma unroll
     for (int nt = 0; nt < 2; ++nt) {
       q.a[nt] *= left[nt];
       left[nt] = q.b[nt];
     }
     uint32_t xw[8];
-    if (GRAD) load16<REV>(chunk_rsrc(a.X, xb, nv, a.dk, 2), xl, a.X.vec, xw);
+    load16<REV>(chunk_rsrc(a.X, xb, nv, a.dk, 2), xl, a.X.vec, xw);
     const Step now = st;
     advance(st);
     const int next = st.pos == kScanC ? c + 1 : c;
@@ -962,57 +947,48 @@ __global__ __launch_bounds__(NW * 64, NV > 4 ? 1 : 2) void scan_grad_kernel(cons
       if (next < nch) fetch(next);   // in flight during the products
     }
     f32x4 o[2][2] = {};
-    if (GRAD) {
-      f32x4 pt[kMine<NW>] = {};   // this wave's W_i . V_j: rows j, columns i
+    f32x4 pt[kMine<NW>] = {};   // this wave's W_i . V_j: rows j, columns i
 #pragma unroll
-      for (int s = 0; s < NV; ++s) {
-        u32x4 wr[2];
-        bf16x8 wt[2][kTerms<DT>];
+    for (int s = 0; s < NV; ++s) {
+      u32x4 wr[2];
+      bf16x8 wt[2][kTerms<DT>];
 #pragma unroll
-        for (int tl = 0; tl < 2; ++tl) {
-          wr[tl] = *(const u32x4*)(ws + row_of(n, tl) * RS + 32 * s + 8 * g);
-          exact_terms<DT>(wr[tl], wt[tl]);
-        }
-#pragma unroll
-        for (int m = 0; m < kMine<NW>; ++m) {
-          int jt, it;
-          score_tile<NW>(wave, m, jt, it);
-          const u32x4 vv = *(const u32x4*)(vs + row_of(n, jt) * RS + 32 * s + 8 * g);
-          const u32x4 wv = *(const u32x4*)(ws + row_of(n, it) * RS + 32 * s + 8 * g);
-          if constexpr (DT == DT_F16)
-            pt[m] = mfma(__builtin_bit_cast(f16x8, vv), __builtin_bit_cast(f16x8, wv), pt[m]);
-          else
-            pt[m] = mfma(__builtin_bit_cast(bf16x8, vv), __builtin_bit_cast(bf16x8, wv), pt[m]);
-        }
-#pragma unroll
-        for (int nt = 0; nt < 2; ++nt) {
-          float x[8];
-          S[s][0][nt] *= q.a[nt];
-          S[s][1][nt] *= q.a[nt];
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            x[r] = S[s][0][nt][r];
-            x[4 + r] = S[s][1][nt][r];
-          }
-          bf16x8 sx[TP];
-          split8<TP>(x, sx);
-#pragma unroll
-          for (int it = 0; it < 2; ++it) o[it][nt] = mfma_terms(wt[it], sx, o[it][nt]);
-        }
+      for (int tl = 0; tl < 2; ++tl) {
+        wr[tl] = *(const u32x4*)(ws + row_of(n, tl) * RS + 32 * s + 8 * g);
+        exact_terms<DT>(wr[tl], wt[tl]);
       }
 #pragma unroll
       for (int m = 0; m < kMine<NW>; ++m) {
         int jt, it;
         score_tile<NW>(wave, m, jt, it);
-        put_scores<TP>(sc, pt[m], jt, it, lane);
+        const u32x4 vv = *(const u32x4*)(vs + row_of(n, jt) * RS + 32 * s + 8 * g);
+        const u32x4 wv = *(const u32x4*)(ws + row_of(n, it) * RS + 32 * s + 8 * g);
+        if constexpr (DT == DT_F16)
+          pt[m] = mfma(__builtin_bit_cast(f16x8, vv), __builtin_bit_cast(f16x8, wv), pt[m]);
+        else
+          pt[m] = mfma(__builtin_bit_cast(bf16x8, vv), __builtin_bit_cast(bf16x8, wv), pt[m]);
       }
-    } else {
 #pragma unroll
-      for (int s = 0; s < NV; ++s)
+      for (int nt = 0; nt < 2; ++nt) {
+        float x[8];
+        S[s][0][nt] *= q.a[nt];
+        S[s][1][nt] *= q.a[nt];
 #pragma unroll
-        for (int tl = 0; tl < 2; ++tl)
+        for (int r = 0; r < 4; ++r) {
+          x[r] = S[s][0][nt][r];
+          x[4 + r] = S[s][1][nt][r];
+        }
+        bf16x8 sx[TP];
+        split8<TP>(x, sx);
 #pragma unroll
-          for (int nt = 0; nt < 2; ++nt) S[s][tl][nt] *= q.a[nt];
+        for (int it = 0; it < 2; ++it) o[it][nt] = mfma_terms(wt[it], sx, o[it][nt]);
+      }
+    }
+#pragma unroll
+    for (int m = 0; m < kMine<NW>; ++m) {
+      int jt, it;
+      score_tile<NW>(wave, m, jt, it);
+      put_scores<TP>(sc, pt[m], jt, it, lane);
     }
 #pragma unroll
     for (int s = 0; s < NV; ++s)
@@ -1026,86 +1002,84 @@ __global__ __launch_bounds__(NW * 64, NV > 4 ? 1 : 2) void scan_grad_kernel(cons
     // from here on the next step may be staged: only the scores are still read,
     // and they are written again behind its own barrier
     __syncthreads();
-    if (GRAD) {
 #pragma unroll
-      for (int it = 0; it < 2; ++it) {
-        bf16x8 ps[TP];
-        get_scores<TP>(sc, it, lane, ps);
+    for (int it = 0; it < 2; ++it) {
+      bf16x8 ps[TP];
+      get_scores<TP>(sc, it, lane, ps);
 #pragma unroll
-        for (int nt = 0; nt < 2; ++nt) {
-          if constexpr (TP == 3) {
-            o[it][nt] = mfma_terms(ps, kk[nt], o[it][nt]);
-          } else {
-            const bf16x8 k2[2] = {kk[nt][0], kk[nt][1]};
-            o[it][nt] = mfma_terms(ps, k2, o[it][nt]);
-          }
-        }
-      }
-      const __amdgpu_buffer_rsrc_t orsrc = chunk_rsrc(a.O, ob, nv, a.dk, 2);
-      const Lane ot = fresh(ol);
-      float y[2][8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float o0 = o[j >> 2][0][j & 3] * q.up[0][j] * a.oscale, o1 = o[j >> 2][1][j & 3] * q.up[1][j] * a.oscale;
-        const bool mine = now.width == 32 || takes(now, g, j);
-        if (mine) store16<REV>(orsrc, ot, a.O.vec, j, pair_round<DT>(o0, o1));
-        y[0][j] = mine ? pair_lo<DT>(xw[j]) * o0 : 0.0f;
-        y[1][j] = mine ? pair_hi<DT>(xw[j]) * o1 : 0.0f;
-      }
-      // the workspace's rows of this chunk: the lane's tokens are rows of H dkp floats
-      float* qr = qdq + tok * a.H * a.dkp + col;
-      const int64_t qs = (int64_t)a.H * a.dkp;
-      if (!REV) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const int i = 8 * g + j;
-          if ((now.width == 32 || takes(now, g, j)) && i < nv && col < a.dkp)
-            *(f32x2*)(qr + i * qs) = f32x2{y[0][j], y[1][j]};
-        }
-      } else {
-        // dg_t = (the value behind the step) + sum over this and the later tokens of q dq - k dk
-        float run[2] = {0.0f, 0.0f}, d[2][8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const int i = 31 - 8 * g - j;
-          f32x2 u = {0.0f, 0.0f};
-          if ((now.width == 32 || takes(now, g, j)) && i < nv && col < a.dkp) u = *(const f32x2*)(qr + i * qs);
-#pragma unroll
-          for (int nt = 0; nt < 2; ++nt) {
-            run[nt] += u[nt] - y[nt][j];
-            d[nt][j] = run[nt];
-          }
-        }
-        const __amdgpu_buffer_rsrc_t drsrc = chunk_rsrc(a.DG, dgb, nv, a.dk, gb);
-        const Lane dt = fresh(dl);
-#pragma unroll
-        for (int nt = 0; nt < 2; ++nt) {
-          float s = run[nt];
-          const float u = __shfl_up(s, 16, 64);
-          if (g >= 1) s += u;
-          const float v = __shfl_up(s, 32, 64);
-          if (g >= 2) s += v;
-          const float before = __shfl_up(s, 16, 64);
-          const float base = (g >= 1 ? before : 0.0f) + carry[nt];
-          carry[nt] += __shfl(s, 48 + n, 64);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) d[nt][j] += base;
-        }
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          if (!(now.width == 32 || takes(now, g, j))) continue;
-          if constexpr (G32) {
-            __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, d[0][j]), drsrc,
-                                                  dt.off0 + tok_off<REV>(dt, j), 0, 0);
-            __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, d[1][j]), drsrc,
-                                                  off1_of<4>(dt) + tok_off<REV>(dt, j), 0, 0);
-          } else {
-            store16<REV>(drsrc, dt, a.DG.vec, j, pair_round<DT>(d[0][j], d[1][j]));
-          }
+      for (int nt = 0; nt < 2; ++nt) {
+        if constexpr (TP == 3) {
+          o[it][nt] = mfma_terms(ps, kk[nt], o[it][nt]);
+        } else {
+          const bf16x8 k2[2] = {kk[nt][0], kk[nt][1]};
+          o[it][nt] = mfma_terms(ps, k2, o[it][nt]);
         }
       }
     }
-    if (GRAD && next != c) {
+    const __amdgpu_buffer_rsrc_t orsrc = chunk_rsrc(a.O, ob, nv, a.dk, 2);
+    const Lane ot = fresh(ol);
+    float y[2][8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float o0 = o[j >> 2][0][j & 3] * q.up[0][j] * a.oscale, o1 = o[j >> 2][1][j & 3] * q.up[1][j] * a.oscale;
+      const bool mine = now.width == 32 || takes(now, g, j);
+      if (mine) store16<REV>(orsrc, ot, a.O.vec, j, pair_round<DT>(o0, o1));
+      y[0][j] = mine ? pair_lo<DT>(xw[j]) * o0 : 0.0f;
+      y[1][j] = mine ? pair_hi<DT>(xw[j]) * o1 : 0.0f;
+    }
+    // the workspace's rows of this chunk: the lane's tokens are rows of H dkp floats
+    float* qr = qdq + tok * a.H * a.dkp + col;
+    const int64_t qs = (int64_t)a.H * a.dkp;
+    if (!REV) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int i = 8 * g + j;
+        if ((now.width == 32 || takes(now, g, j)) && i < nv && col < a.dkp)
+          *(f32x2*)(qr + i * qs) = f32x2{y[0][j], y[1][j]};
+      }
+    } else {
+      // dg_t = (the value behind the step) + sum over this and the later tokens of q dq - k dk
+      float run[2] = {0.0f, 0.0f}, d[2][8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int i = 31 - 8 * g - j;
+        f32x2 u = {0.0f, 0.0f};
+        if ((now.width == 32 || takes(now, g, j)) && i < nv && col < a.dkp) u = *(const f32x2*)(qr + i * qs);
+#pragma unroll
+        for (int nt = 0; nt < 2; ++nt) {
+          run[nt] += u[nt] - y[nt][j];
+          d[nt][j] = run[nt];
+        }
+      }
+      const __amdgpu_buffer_rsrc_t drsrc = chunk_rsrc(a.DG, dgb, nv, a.dk, gb);
+      const Lane dt = fresh(dl);
+#pragma unroll
+      for (int nt = 0; nt < 2; ++nt) {
+        float s = run[nt];
+        const float u = __shfl_up(s, 16, 64);
+        if (g >= 1) s += u;
+        const float v = __shfl_up(s, 32, 64);
+        if (g >= 2) s += v;
+        const float before = __shfl_up(s, 16, 64);
+        const float base = (g >= 1 ? before : 0.0f) + carry[nt];
+        carry[nt] += __shfl(s, 48 + n, 64);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) d[nt][j] += base;
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        if (!(now.width == 32 || takes(now, g, j))) continue;
+        if constexpr (G32) {
+          __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, d[0][j]), drsrc,
+                                                dt.off0 + tok_off<REV>(dt, j), 0, 0);
+          __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, d[1][j]), drsrc,
+                                                off1_of<4>(dt) + tok_off<REV>(dt, j), 0, 0);
+        } else {
+          store16<REV>(drsrc, dt, a.DG.vec, j, pair_round<DT>(d[0][j], d[1][j]));
+        }
+      }
+    }
+    if (next != c) {
       walk<REV>(a.X, xb, 2);
       walk<REV>(a.O, ob, 2);
       if (REV) walk<REV>(a.DG, dgb, gb);
@@ -1120,24 +1094,6 @@ __global__ __launch_bounds__(NW * 64, NV > 4 ? 1 : 2) void scan_grad_kernel(cons
     for (int tl = 0; tl < 2; ++tl)
 #pragma unroll
       for (int nt = 0; nt < 2; ++nt) S[s][tl][nt] *= left[nt];
-  if (!GRAD) {
-    // this segment's own state, from zero
-#pragma unroll
-    for (int s = 0; s < NV; ++s)
-#pragma unroll
-      for (int tl = 0; tl < 2; ++tl)
-#pragma unroll
-        for (int nt = 0; nt < 2; ++nt) {
-          const int e = 32 * s + 8 * g + 4 * tl;
-          if (col + nt < a.dkp && a.ecol + e < a.dvp)
-            *(f32x4*)(slot + (int64_t)(col + nt) * a.dvp + a.ecol + e) = S[s][tl][nt];
-        }
-    if (g == 0)
-#pragma unroll
-      for (int nt = 0; nt < 2; ++nt)
-        if (col + nt < a.dkp) a.decays[p.slot * a.dkp + col + nt] = all_decay[nt];
-    return;
-  }
   if (REV) {
     if (a.ST && p.seg == 0) {
 #pragma unroll
@@ -1181,6 +1137,191 @@ __global__ __launch_bounds__(NW * 64, NV > 4 ? 1 : 2) void scan_grad_kernel(cons
       if (g == 0 && col + nt < a.dkp) a.ends[p.slot * a.dkp + col + nt] = w[nt];
     }
   }
+}
+
+// ---- a segment's own state ----------------------------------------------------
+// From zero, S = sum_t k_t e^{the gates behind t} v_t^T (reversed: q_t do_t^T and
+// the gates before it and its own).  The tokens are walked against the order of
+// the recurrence, so a token's factor is the running product of what has been
+// walked and the sums are never rescaled: no chunk is cut for its gates' sake,
+// and a factor that underflows belongs to a contribution that has decayed.
+// Where that does not hold -- factors or values beyond kBig, or factors that
+// rise again after they were tiny -- the wave does its channels over again as
+// the recurrence itself.
+
+template <int NV>
+constexpr size_t scan_state_lds() {
+  return (size_t)2 * NV * 32 * kTokRow * 2;
+}
+constexpr float kTiny = 0x1p-110f;  // factors that get close to float32's end lose bits
+constexpr float kRise = 20.0f;      // which matter if they can rise by e^kRise (2^29) again
+
+template <int DT, bool G32, int NV, int NW, bool REV>
+__device__ __forceinline__ void own_state(const ScanArgs& a) {
+  constexpr int DVP = NV * 32;
+  constexpr int gb = G32 ? 4 : 2;
+  constexpr int SL = (NV + NW - 1) / NW;        // slabs of 32 columns a wave stages
+  constexpr bool DIR = !REV;                    // the order of the walk
+  extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
+
+  Place p;
+  if (!place_of(a, p)) return;
+  // the state at the far end is not a start of any segment
+  if (REV ? p.seg == 0 : p.last) return;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int n = lane & 15, g = lane >> 4;
+  const int col = (p.blk * NW + wave) * 32 + 2 * n;       // the lane's channels col, col + 1
+
+  const char *kb = base_of<DIR>(a.K, p, 2), *vb = base_of<DIR>(a.V, p, 2), *gbp = base_of<DIR>(a.G, p, gb);
+  const Lane kl = lane_of<DIR>(a.K, g, col, a.dk, 2), gl = lane_of<DIR>(a.G, g, col, a.dk, gb);
+  Lane vl[SL];
+#pragma unroll
+  for (int i = 0; i < SL; ++i) vl[i] = lane_of<DIR>(a.V, g, 32 * (wave + i * NW) + 2 * n, a.dv, 2);
+  const int nch = (int)((p.hi - p.lo + kScanC - 1) / kScanC);
+  uint32_t kw[8], gw[kGateWords<G32>], vw[SL][8];
+  auto fetch = [&](int c) {
+    const int64_t tok = p.lo + (int64_t)(DIR ? nch - 1 - c : c) * kScanC;
+    const int nv = (int)min((int64_t)kScanC, p.hi - tok);
+    const auto vr = chunk_rsrc(a.V, vb, nv, a.dv, 2);
+#pragma unroll
+    for (int i = 0; i < SL; ++i) load16<DIR>(vr, vl[i], a.V.vec, vw[i]);
+    load_gates<DIR, G32>(chunk_rsrc(a.G, gbp, nv, a.dk, gb), gl, a.G.vec, gw);
+    load16<DIR>(chunk_rsrc(a.K, kb, nv, a.dk, 2), kl, a.K.vec, kw);
+    walk<DIR>(a.V, vb, 2);
+    walk<DIR>(a.G, gbp, gb);
+    walk<DIR>(a.K, kb, 2);
+  };
+  if (nch > 0) fetch(0);
+  f32x4 S[NV][2][2] = {};               // rows: DV, columns: the lane's channels
+  float run[2] = {1.0f, 1.0f};          // the walked gates' decay
+  float low = 1.0f, rise = 0.0f, big = 0.0f;
+  for (int c = 0; c < nch; ++c) {
+    uint16_t* vt = (uint16_t*)smem + (c & 1) * DVP * kTokRow;   // V transposed [DVP][kTokRow]
+#pragma unroll
+    for (int i = 0; i < SL; ++i) {
+      const int s = wave + i * NW, e0 = 32 * s + 2 * n;
+      if (NV % NW != 0 && s >= NV) break;
+      u32x4 c0, c1;
+      columns_of(vw[i], c0, c1);
+      *(u32x4*)(vt + e0 * kTokRow + 8 * g) = c0;
+      *(u32x4*)(vt + (e0 + 1) * kTokRow + 8 * g) = c1;
+    }
+    bf16x8 kk[2][3];
+    float top = 0.0f;
+#pragma unroll
+    for (int ch = 0; ch < 2; ++ch) {
+      float P[8], of = 1.0f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float x = gate_value<DT, G32>(gw, ch, j);
+        top = __builtin_fmaxf(top, x);
+        const float e = __builtin_amdgcn_exp2f(x * 1.44269504f);
+        if (DIR) P[j] = of;
+        of = j == 0 ? e : of * e;
+        if (!DIR) P[j] = of;
+      }
+      // times the groups walked before this one, and the chunks before
+      const float next = __shfl_xor(of, 16, 64), both = of * next;
+      const float other = __shfl_xor(both, 32, 64);
+      const float f = run[ch] * ((g & 1 ? next : 1.0f) * (g & 2 ? other : 1.0f));
+      run[ch] *= both * other;
+      float kf[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float x = P[j] * f;
+        low = __builtin_fminf(low, x);
+        kf[j] = (ch ? pair_hi<DT>(kw[j]) : pair_lo<DT>(kw[j])) * x;
+        if (REV) kf[j] *= a.kscale;
+        big += __builtin_fabsf(kf[j]);
+      }
+      split8<3>(kf, kk[ch]);
+      if (!(run[ch] <= kBig)) big = __builtin_inff();   // NaN too
+    }
+    rise += 8.0f * top;
+    // one buffer is staged while the other is read: its last readers are behind
+    // the barrier before this one
+    __syncthreads();
+    if (c + 1 < nch) fetch(c + 1);   // in flight during the products
+#pragma unroll
+    for (int s = 0; s < NV; ++s)
+#pragma unroll
+      for (int tl = 0; tl < 2; ++tl) {
+        bf16x8 vv[kTerms<DT>];
+        exact_terms<DT>(*(const u32x4*)(vt + (32 * s + row_of(n, tl)) * kTokRow + 8 * g), vv);
+#pragma unroll
+        for (int nt = 0; nt < 2; ++nt) S[s][tl][nt] = mfma_terms(vv, kk[nt], S[s][tl][nt]);
+      }
+  }
+
+  rise += __shfl_xor(rise, 16, 64);   // of all the chunk's tokens
+  rise += __shfl_xor(rise, 32, 64);
+  low = __builtin_fminf(low, __shfl_xor(low, 16, 64));
+  low = __builtin_fminf(low, __shfl_xor(low, 32, 64));
+  if (__ballot(!(big <= kBig) || (rise > kRise && low < kTiny))) {
+    const char *k1 = (const char*)a.K.p, *v1 = (const char*)a.V.p, *g1 = (const char*)a.G.p;
+    run[0] = run[1] = 1.0f;
+#pragma unroll
+    for (int s = 0; s < NV; ++s)
+#pragma unroll
+      for (int tl = 0; tl < 2; ++tl) S[s][tl][0] = S[s][tl][1] = f32x4{};
+    for (int64_t i = 0; i < p.hi - p.lo; ++i) {
+      const int64_t tok = p.row0 + (REV ? p.hi - 1 - i : p.lo + i);
+      const uint16_t* kr = (const uint16_t*)k1 + (p.b * a.K.sb + p.h * a.K.sh + tok * a.K.st);
+      const uint16_t* vr = (const uint16_t*)v1 + (p.b * a.V.sb + p.h * a.V.sh + tok * a.V.st);
+      const char* gr = g1 + (p.b * a.G.sb + p.h * a.G.sh + tok * a.G.st) * gb;
+      float ex[2], k[2];
+#pragma unroll
+      for (int nt = 0; nt < 2; ++nt) {
+        ex[nt] = 1.0f;
+        k[nt] = 0.0f;
+        if (col + nt < a.dk) {
+          k[nt] = widen<DT>(kr[col + nt]) * (REV ? a.kscale : 1.0f);
+          ex[nt] = expf(G32 ? ((const float*)gr)[col + nt] : widen<DT>(((const uint16_t*)gr)[col + nt]));
+        }
+        run[nt] *= ex[nt];
+      }
+#pragma unroll
+      for (int s = 0; s < NV; ++s)
+#pragma unroll
+        for (int tl = 0; tl < 2; ++tl)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const int e = 32 * s + 8 * g + 4 * tl + r;
+            const float v = e < a.dv ? widen<DT>(vr[e]) : 0.0f;
+#pragma unroll
+            for (int nt = 0; nt < 2; ++nt) {
+              const float x = S[s][tl][nt][r];
+              S[s][tl][nt][r] = REV ? __builtin_fmaf(k[nt], v, x) * ex[nt] : __builtin_fmaf(k[nt], v, x * ex[nt]);
+            }
+          }
+    }
+  }
+
+  float* slot = a.slots + p.slot * (int64_t)a.dkp * a.dvp;
+#pragma unroll
+  for (int s = 0; s < NV; ++s)
+#pragma unroll
+    for (int tl = 0; tl < 2; ++tl)
+#pragma unroll
+      for (int nt = 0; nt < 2; ++nt) {
+        const int e = 32 * s + 8 * g + 4 * tl;
+        if (col + nt < a.dkp && a.ecol + e < a.dvp)
+          *(f32x4*)(slot + (int64_t)(col + nt) * a.dvp + a.ecol + e) = S[s][tl][nt];
+      }
+  if (g == 0)
+#pragma unroll
+    for (int nt = 0; nt < 2; ++nt)
+      if (col + nt < a.dkp) a.decays[p.slot * a.dkp + col + nt] = run[nt];
+}
+
+// The two recurrences of a backward pass side by side (grid y), or the forward one alone.
+struct StateArgs {
+  ScanArgs fwd, rev;
+};
+template <int DT, bool G32, int NV, int NW>
+__global__ __launch_bounds__(NW * 64, 2) void scan_state_kernel(const StateArgs a) {
+  if (blockIdx.y == 0) own_state<DT, G32, NV, NW, false>(a.fwd);
+  else own_state<DT, G32, NV, NW, true>(a.rev);
 }
 
 }  // namespace mbd

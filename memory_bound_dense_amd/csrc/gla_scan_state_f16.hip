@@ -1,10 +1,10 @@
-// libmbd_operators.so: the f16 forms of scan_grad_kernel that leave a segment's own state.
+// libmbd_operators.so: the f16 forms of scan_state_kernel.
 #include "gla_scan_table.h"
 
 namespace mbd {
 
-#define FORM(G32, N, REV) {&scan_grad_kernel<DT_F16, G32, N, 2, REV, false>, &scan_grad_kernel<DT_F16, G32, N, 4, REV, false>}
-#define FORMS(G32, REV) {FORM(G32, 2, REV), FORM(G32, 4, REV), FORM(G32, 8, REV)}
-extern const ScanForms kScanStateF16 = {{FORMS(false, false), FORMS(false, true)}, {FORMS(true, false), FORMS(true, true)}};
+#define FORM(G32, N) {&scan_state_kernel<DT_F16, G32, N, 2>, &scan_state_kernel<DT_F16, G32, N, 4>}
+extern const StateForms kScanStateF16 = {{FORM(false, 2), FORM(false, 4), FORM(false, 8)},
+                                         {FORM(true, 2), FORM(true, 4), FORM(true, 8)}};
 
 }  // namespace mbd

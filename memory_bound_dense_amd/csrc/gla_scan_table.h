@@ -9,8 +9,10 @@ namespace mbd {
 
 using ScanFn = void (*)(const ScanArgs);
 using ScanForms = ScanFn[2][2][3][2];
+using StateFn = void (*)(const StateArgs);   // both directions in one
+using StateForms = StateFn[2][3][2];
 extern const ScanForms kScanOutF16, kScanOutBf16;       // channels: DK
 extern const ScanForms kScanGradF16, kScanGradBf16;     // channels: DV
-extern const ScanForms kScanStateF16, kScanStateBf16;   // channels: DV
+extern const StateForms kScanStateF16, kScanStateBf16;   // channels: DV
 
 }  // namespace mbd

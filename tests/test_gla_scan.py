@@ -48,7 +48,11 @@ def cuda(x):
 def step(dt):
     """(relative, absolute) half step of a 16-bit type."""
     f = torch.finfo(dt)
-    return (0.0, 0.0) if dt == F32 else (f.eps / 2, f.smallest_normal * f.eps / 2)
+    # float32 results carry no rounding of their own, but below 2^-126 a rounding is up to 2^-150
+    # whatever the value: a state takes three per chunk (two scalings, a sum), those of earlier
+    # chunks decayed by the chunks since.  States only get there by decays, at the least e^-1.4 a
+    # chunk here: 3 / (1 - e^-1.4) < 4 of them.
+    return (0.0, 4 * 2.0 ** -150) if dt == F32 else (f.eps / 2, f.smallest_normal * f.eps / 2)
 
 
 def close(name, got, want, bound, dt):
@@ -87,27 +91,28 @@ def bwd(scan, x, offsets=None, longest=None):
     return r
 
 
-def check_fwd(x, o, ST, seq, rows, out=0):
-    """Sequence `seq` (state index `out`) at rows `rows` of batch entry 0 or seq."""
+def check_fwd(x, o, ST, seq, rows, out=0, floor=0.0):
+    """Sequence `seq` (state index `out`) at rows `rows` of batch entry 0 or seq.  floor: an
+    absolute error on top, for results below the normal range."""
     a = [f64(x[n][seq, rows]) for n in ("q", "k", "v", "g")]
     S0 = None if x["S0"] is None else f64(x["S0"][out])
     wo, wS, ao, aS = scan_ref.forward(*a, x["scale"], S0)
     t = a[0].shape[0]
-    close("o", o[seq, rows], wo, scan_ref.rel16(t, a[3]) * ao, o.dtype)
+    close("o", o[seq, rows], wo, scan_ref.rel16(t, a[3]) * ao + floor, o.dtype)
     close("ST", ST[out], wS, scan_ref.rel32(t, a[3]) * aS, F32)
 
 
-def check_bwd(x, r, seq, rows, out=0):
+def check_bwd(x, r, seq, rows, out=0, floor=0.0):
     a = [f64(x[n][seq, rows]) for n in ("q", "k", "v", "g", "do")]
     S0, dST = (None if x[n] is None else f64(x[n][out]) for n in ("S0", "dST"))
     want, ab = scan_ref.backward(*a, x["scale"], S0, dST)
     t, g = a[0].shape[0], a[3]
     for n in ("dq", "dk", "dv"):
-        close(n, r[n][seq, rows], want[n], scan_ref.rel16(t, g) * ab[n], x["q"].dtype)
+        close(n, r[n][seq, rows], want[n], scan_ref.rel16(t, g) * ab[n] + floor, x["q"].dtype)
     # a sum of q dq - k dk: with float32 gates both come from three-term factors (the bound of
     # a float32 result on each term), with 16-bit gates from two-term ones
     rel = scan_ref.rel32(t, g) if x["g"].dtype == F32 else scan_ref.rel16(t, g)
-    close("dg", r["dg"][seq, rows], want["dg"], 2 * rel * ab["dg_run"], x["g"].dtype)
+    close("dg", r["dg"][seq, rows], want["dg"], 2 * rel * ab["dg_run"] + 10 * t * floor, x["g"].dtype)
     close("dS0", r["dS0"][out], want["dS0"], scan_ref.rel32(t, g) * ab["dS0"], F32)
 
 
@@ -166,6 +171,52 @@ def test_gates_of_every_size(scan, kind, t, dk, dv, dt, gt):
     o, ST = fwd(scan, x)
     check_fwd(x, o, ST, 0, slice(None))
     check_bwd(x, bwd(scan, x), 0, slice(None))
+
+
+@pytest.mark.parametrize("kind", ["decaying", "resets", "overflow", "rise"])
+@pytest.mark.parametrize("gt", [BF, F32], ids=["bf16", "f32gate"])
+def test_long_segments(scan, kind, gt):
+    """256 heads of the same data (head stride 0): segments of 256 tokens, whose own states are
+    summed from their ends.  overflow: 100 gates of 1.2 over states of zeros (e^120 is beyond
+    float32); rise: 80 gates of 1, then 60 of -2, over contributions from before them."""
+    t, h, d = 1024, 256, 32
+    x = inputs(1, t, 1, d, d, BF, gt, gate=8.0, seed=5, state=kind in ("decaying", "resets"))
+    if kind == "resets":
+        x["g"][0, 300, 0, ::3] = -math.inf
+        x["g"][0, 511:513, 0, 1::3] = -math.inf
+        x["g"][0, 256, 0, 2::6] = -math.inf
+    elif kind == "overflow":
+        x["g"][0, 300:400] = 1.2
+        x["k"][0, :400] = 0
+        x["q"][0, 300:] = 0
+    elif kind == "rise":
+        x["g"][0, 276:356] = 1.0
+        x["g"][0, 436:496] = -2.0
+        x["k"][0, 276:] = 0
+        x["q"][0, 436:] = 0
+    many = {n: v.expand(1, t, h, d) if torch.is_tensor(v) and v.dim() == 4 and n not in ("S0", "dST")
+            else v for n, v in cuda(x).items()}
+    for n in ("S0", "dST"):
+        if x[n] is not None:
+            many[n] = many[n].expand(1, h, d, d).contiguous()
+    full = lambda dt, *s: torch.full(s, float("nan"), dtype=dt, device="cuda")
+    o, ST = full(BF, 1, t, h, d), full(F32, 1, h, d, d)
+    scan.forward(many["q"], many["k"], many["v"], many["g"], o, x["scale"], S0=many["S0"], ST=ST)
+    r = {n: full(gt if n == "dg" else BF, 1, t, h, d) for n in ("dq", "dk", "dv", "dg")}
+    r["dS0"] = full(F32, 1, h, d, d)
+    scan.backward(many["q"], many["k"], many["v"], many["g"], many["do"], r["dq"], r["dk"], r["dv"], r["dg"],
+                  x["scale"], S0=many["S0"], dST=many["dST"], dS0=r["dS0"])
+    torch.cuda.synchronize()
+    for y in (o, *[r[n] for n in ("dq", "dk", "dv", "dg")]):
+        assert torch.equal(y, y[:, :, :1].expand_as(y))
+    # "rise" ends in states of 2^-140.  An element below 2^-126 goes into the products as bf16 terms
+    # of step 2^-133, so with an error of up to 2^-134, times a sum over 32 channels of |q|, |do|,
+    # |v| or |k| (each below 5): 2^-134 * 160.  The gates' gradient sums q dq - k dk, two such
+    # errors times 5, over t tokens.
+    assert all(x[n].abs().max() < 5 for n in ("q", "k", "v", "do")) and x["scale"] < 1
+    floor = 160 * 2.0 ** -134
+    check_fwd(x, o[:, :, :1], ST[:, :1], 0, slice(None), floor=floor)
+    check_bwd(x, {n: y[:, :, :1] if n != "dS0" else y[:, :1] for n, y in r.items()}, 0, slice(None), floor=floor)
 
 
 @pytest.mark.parametrize("what", ["q", "k", "v", "do", "g"])
