@@ -95,11 +95,14 @@ int out_cols(int64_t dv) {   // output columns per workgroup: even shares of at 
 // leave the GPU idle: as many as fit it in one round (two workgroups of four
 // waves a CU, or four of two; a few more than that take a second round: 156
 // heads and blocks in 4 segments of 400 tokens 173 us, in 3 127), of at least
-// 64 tokens (forward; the segments' own states are a pass of their own) or 32
-// (backward).  Measured forward, 32 heads of 128 x 128, 512 tokens: segments of
-// 64 / 128 / 256 tokens 48 / 59 / 79 us; 129 tokens: whole 32 us, in segments of
-// 64 or 96 39..43.  Backward, 15 heads of 64 x 96, 1001 tokens: segments of 32 /
-// 64 / 160 / 256 tokens 113 / 136 / 187 / 344 us.
+// 64 tokens, or 32 where that leaves most of the round free (forward three
+// quarters, backward half); short sequences stay whole, since the segments' own
+// states are passes of their own.  Measured, heads of 128 x 128, in us (whole /
+// segments of 32 / of 64):
+//   forward   8 heads   129 tokens 28 / 29 / 33    255 41 / 31 / 34    512 77 / 38 / 37
+//            32 heads   192        32 / 38 / 37    255 41 / 39 / 39    512 78 / 45 / 43
+//   backward  8 heads    96        64 / 47 / 62   1001 517 / 79 / 85  1500 753 / 99 / 91
+//            32 heads    64        48 / 50 / 49    255 144 / 74 / 82   512 284 / 106 / 95
 ScanPlan scan_plan(const gla_scan_t* p, bool backward) {
   ScanPlan s = {};
   s.dkp = (int32_t)up(p->dk, 32);
@@ -108,9 +111,11 @@ ScanPlan scan_plan(const gla_scan_t* p, bool backward) {
   const int64_t width = backward ? p->dk : out_cols(p->dv);
   const int waves = waves_of(width);
   const int64_t blocks = backward ? (p->dk + 32 * waves - 1) / (32 * waves) : (p->dv + width - 1) / width;
-  const int64_t room = 2048 / waves / std::max(s.heads * blocks, (int64_t)1);
-  int64_t nseg = std::min(room, p->tokens / (backward ? 32 : 64));
-  if (p->tokens < (backward ? 128 : 256)) nseg = 1;
+  const int64_t slots = 2048 / waves, units = std::max(s.heads * blocks, (int64_t)1);
+  const bool fine = units * ((p->tokens + 31) / 32) <= slots / (backward ? 2 : 4);
+  const int64_t least = fine ? 32 : 64;
+  int64_t nseg = std::min(slots / units, (p->tokens + least - 1) / least);
+  if (p->tokens < (backward ? 96 : fine ? 160 : 224)) nseg = 1;
   nseg = std::max(nseg, (int64_t)1);
   const int64_t L = std::max(up((p->tokens + nseg - 1) / nseg, mbd::kScanC), (int64_t)mbd::kScanC);
   s.L = (int)L;
