@@ -12,7 +12,9 @@ namespace mbd {
 // ---- segments' states from their own states ----------------------------------
 // slots[s] holds segment s's own state (from zero; the last segment's in the
 // order of the recurrence is not there, and not needed) and becomes its start
-// state: one thread per 4 elements walks the sequence's segments.
+// state: one thread per 4 elements walks the sequence's segments.  Bound by HBM
+// (64 heads of 128 x 128, 8 segments: 63 MB in 10.4 us, 6.0 TB/s) and, for few
+// heads, by the walk (15 heads of 64 x 96, 16 segments, both sides: 10 us).
 struct Join {
   float* slots;
   const float* decays;

@@ -11,25 +11,27 @@
 //
 // (the last because rowsum(S_t D_t) = dg_t + k_t dk_t = dg_{t+1} + q_t dq_t).
 // Reversed, a recurrence differs from the forward one only in its order and
-// in that a token's gate acts after the token instead of before it, so two
-// kernels serve everything:
+// in that a token's gate acts after the token instead of before it, so the same
+// kernels serve both:
+//   scan_state_kernel  a segment's own state
 //   scan_out_kernel    out_i  = X_i^T S     o  (K k, V v, X q), dv (K q, V do, X k)
 //   scan_grad_kernel   out_i  = S W_i       dq (K k, V v, W do), dk (K q, V do, W v)
 //
 // A chunk of 32 tokens is one step.  With G the running sum of the gates in
 // the chunk and r its value at the middle, the chunk is matrix products of
 // x e^{G-r} and k e^{r-G}: their product is the decay e^{G_i - G_j} of every
-// pair, and |G - r| <= kRange keeps each factor far from overflow.  Chunks
-// where it does not hold (very strong gates, gates of -inf that clear the
-// state) and chunks with values that are not finite take the recurrence
-// itself, token by token, in the same registers; there a masked pair is
-// never formed, so nothing leaks from a later token into an earlier one.
+// pair, and |G - r| <= kRange keeps each factor far from overflow.  Where that
+// does not hold (very strong gates, gates of -inf that clear the state) or a
+// value is not finite, the same code takes the chunk 8 tokens at a time, and
+// where it still does not, one token at a time, whose decay acts as a whole on
+// the state: no pair of factors is formed, so any gate will do and nothing
+// leaks from a later token into an earlier one.
 //
 // Precision: the products run on bf16 matrix instructions with fp32 sums, and
 // every fp32 factor enters as a sum of bf16 terms -- two (2^-17 relative) where
 // the result is rounded to 16 bits right after, three (2^-25) where it goes
-// into the fp32 state or the gates' gradient, which is a difference of sums.
-// q, k, v and do are exact in one term (bf16) or two (f16).
+// into the fp32 state or a float32 gradient of the gates, which is a difference
+// of sums.  q, k, v and do are exact in one term (bf16) or two (f16).
 //
 // Layout.  16x16x32 matrix instructions: an operand's lane (n = lane & 15,
 // g = lane >> 4) holds row/column n and the 8 depth positions 8g..8g+7; a
@@ -57,7 +59,7 @@ typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
 constexpr int kScanC = 32;               // tokens per chunk
 constexpr float kRange = 40.0f;          // largest |G - r| of a chunk done as products
-constexpr float kBig = 1e37f;            // chunks with larger factors are done token by token
+constexpr float kBig = 1e37f;            // steps with larger factors are made smaller
 
 // A (sequence, token, head, channel) tensor: element strides, channels dense.
 struct ScanTensor {
@@ -488,9 +490,21 @@ __device__ __forceinline__ void get_scores(const uint8_t* ps, int it, int lane, 
 }
 
 // ---- out_i = X_i^T S ---------------------------------------------------------
-// A wave owns 32 columns of the state (64 VGPRs at DK 128) and of the output;
-// X e^{G-r} and K e^{r-G} are computed once per workgroup, 32 channels per
-// wave, and shared through LDS as bf16 terms.
+// With S the state before the chunk, in units of e^{-r}:
+//     out = X' S + tril(X' K'^T) V,  S <- S + K'^T V,  X' = X e^{G-r}, K' = K e^{r-G}
+// (reversed the diagonal of the decays belongs to the pair's later token).  A
+// wave owns 32 columns of the state (64 VGPRs at DK 128) and of the output; X'
+// and K' are computed once per workgroup, 32 channels per wave, and shared
+// through LDS as bf16 terms, K' also transposed for the state's update.  Two
+// barriers a chunk, the next chunk's loads in flight between them.
+//
+// Bound by issue and latency at two waves a SIMD: 4 x 2048 tokens, 16 heads of
+// 128 x 128 in 8 segments take 75 us (168 MB: 2.2 TB/s; 7.4 us per further chunk
+// of all 512 workgroups: 2.8 TB/s), vector units busy half of the time, matrix
+// units a quarter.  Three workgroups a CU spill (154 us for 122 in all), and
+// transposing LDS reads, rows without bank conflicts and operands read ahead
+// change nothing: no part of a chunk's work weighs more than 10 us.  One lone
+// workgroup takes 4.4 us a chunk, which bounds short sequences of few heads.
 
 template <int NS>
 constexpr size_t scan_out_lds() {
@@ -770,10 +784,13 @@ __global__ __launch_bounds__(NW * 64, NS > 4 ? 1 : 2) void scan_out_kernel(const
 }
 
 // ---- out_i = S W_i ------------------------------------------------------------
+// out_i = e^{G_i - r} (S W_i + sum_j tril(W_i . V_j) K'_j), and with it dg.
 // A wave owns 32 channels (columns of the transposed state, 64 VGPRs at DV
 // 128) and their part of the output; K e^{r-G} of its channels never leaves
 // its registers.  V and W go through LDS, row-major for the products over DV
-// and V also transposed for the state's update.
+// and V also transposed for the state's update.  At the sizes above: dq 90 us
+// with q dq left in float32 for the gates' gradient (235 MB: 2.6 TB/s), dk with
+// dg 103 us (270 MB), bound as above.
 
 template <int NV>
 constexpr size_t scan_grad_lds() {
@@ -1147,7 +1164,9 @@ __global__ __launch_bounds__(NW * 64, NV > 4 ? 1 : 2) void scan_grad_kernel(cons
 // and a factor that underflows belongs to a contribution that has decayed.
 // Where that does not hold -- factors or values beyond kBig, or factors that
 // rise again after they were tiny -- the wave does its channels over again as
-// the recurrence itself.
+// the recurrence itself.  K and its factors stay in a wave's registers, V is
+// shared through LDS in two buffers, one barrier a chunk.  Bound by HBM: at the
+// sizes above 27 us (88 MB read, 29 MB written: 4.3 TB/s; further chunks at 5.1).
 
 template <int NV>
 constexpr size_t scan_state_lds() {
