@@ -219,6 +219,7 @@ extern "C" gemv_status_t gemm_run(gemv_handle_t h, const gemm_t* p, const void* 
   a.tiles_n = (int32_t)g.tiles_n;
   a.nsplit = (int32_t)g.nsplit;
   a.npad = (int32_t)g.npad;
+  a.once = (((uintptr_t)B | (uint64_t)a.ldb) & 127u) == 0;
   a.alpha = p->alpha;
   const int64_t grid = g.tiles_m * g.tiles_n * g.nsplit;
   const int threads = g.tile ? g.tile->threads : kSkinnyWaves * 64;

@@ -47,6 +47,7 @@ struct GemmArgs {
   int32_t m, n, kbytes;
   int32_t act, out, vec;    // out: DT_F16 / DT_BF16; vec: C and residual rows take 8-byte accesses
   int32_t tiles_m, tiles_n, nsplit, npad;
+  int32_t once;             // few tokens: slabs of B are whole lines, fetched once
   float alpha;
 };
 
@@ -285,7 +286,10 @@ __device__ __forceinline__ void write_tile(const GemmArgs& p, const f32x4 (&c)[T
 // each, and stop at 3.0 TB/s whatever the depth.  U slabs are kept in flight.
 // Bound by HBM: 16 tokens, n = 11008, k = 4096 in bf16 with cold weights 17.2 us
 // (5.2 TB/s, what a large copy reaches).  A ring of 4 slabs and 16 waves were
-// slower.
+// slower.  Rows that do not begin on a line share each line between two slabs:
+// then lines are kept for the next one (16 tokens, n = 4097, k = 4099: 13.4 us
+// for 19.1; n = 18432, k = 7169: 85 for 91), which costs where they are not
+// shared (n = 18432, k = 7168: 55 for 52).
 
 template <int IN, int RT, int MT, int W, int U>
 __global__ __launch_bounds__(W * 64) void gemm_skinny_kernel(const GemmArgs p) {
@@ -354,7 +358,9 @@ __global__ __launch_bounds__(W * 64) void gemm_skinny_kernel(const GemmArgs p) {
   auto fetch = [&](Slab& to, int at) {
     const uint32_t o = (uint32_t)at * 128;
 #pragma unroll
-    for (int i = 0; i < 2 * RT; ++i) to.b[i] = __builtin_amdgcn_raw_buffer_load_b128(br, boff[i] + o, 0, 2);   // no reuse
+    for (int i = 0; i < 2 * RT; ++i)
+      to.b[i] = p.once ? __builtin_amdgcn_raw_buffer_load_b128(br, boff[i] + o, 0, 2)
+                       : __builtin_amdgcn_raw_buffer_load_b128(br, boff[i] + o, 0, 0);
 #pragma unroll
     for (int i = 0; i < MT * 2; ++i) to.a[i] = __builtin_amdgcn_raw_buffer_load_b128(ar, aoff[i] + o, 0, 0);
   };
