@@ -8,11 +8,16 @@ For every result the reference also returns the same sum over absolute values
 Bounds (u = 2^-24, the fp32 half step).  A 16-bit result is rounded once:
 eps/2 |x|.  Before that, every term of a sum has passed through: factors held
 as two bf16 terms, each within 2^-17 (X e^{G-r}, K e^{r-G}, the score, the
-state: 4 * 2^-17 = 2^-15); the exponentials of chunk sums G, each of at most 11
-roundings of |G| <= gmax, twice: 24 u gmax; fp32 sums over at most 256 + 32
-terms, in matrix instructions of 32 terms each and a tree inside: at most
-16 u + 32 u; and for the part that comes from earlier chunks one such decay
-and three roundings (two scalings, one add) per chunk.  Together
+state: 4 * 2^-17 = 2^-15); a decay over a chunk, a product of at most 32
+exponentials: the argument x log2(e) is within u |x| log2(e) twice over (the
+constant and the product), so the exponentials together within 2 u gmax, where
+24 u gmax are allowed, and beside that each is within one unit (2 u) and
+enters with one rounding, 32 * 3 u if all had one sign and below 3 sqrt(32) u =
+17 u as the independent errors that they are, twice (a pair's two factors, or
+a chunk's two halves): 34 u; fp32 sums over at most 256 + 32 terms, in matrix
+instructions of 32 terms each with a tree inside: at most 16 u; and for the
+part that comes from earlier chunks one such decay and two roundings (the
+scaling, the sum) per chunk: 34 + 16 + 2 = 52.  Together
     REL16 = 2^-15 + (chunks + 1) * (24 gmax + 52) u
 Results kept in float32 (states, their gradients) come from three-term factors
 (2^-25 each): REL32 = (chunks + 1) * (24 gmax + 52) u + 2^-24.
