@@ -288,8 +288,10 @@ ScanFn scan_form(const ScanForms* const (&forms)[2], const gla_scan_t* p, int re
   return (*forms[p->dtype])[p->gate_f32][rev][tier][four];
 }
 const size_t kOutLds[3] = {mbd::scan_out_lds<2>(), mbd::scan_out_lds<4>(), mbd::scan_out_lds<8>()};
-const size_t kStateLds[3] = {mbd::scan_state_lds<2>(), mbd::scan_state_lds<4>(), mbd::scan_state_lds<8>()};
-const size_t kGradLds[3] = {mbd::scan_grad_lds<2>(), mbd::scan_grad_lds<4>(), mbd::scan_grad_lds<8>()};
+template <int DT> constexpr size_t kStateLdsOf[3] = {mbd::scan_state_lds<DT, 2>(), mbd::scan_state_lds<DT, 4>(), mbd::scan_state_lds<DT, 8>()};
+template <int DT> constexpr size_t kGradLdsOf[3] = {mbd::scan_grad_lds<DT, 2>(), mbd::scan_grad_lds<DT, 4>(), mbd::scan_grad_lds<DT, 8>()};
+size_t state_lds(int dtype, int t) { return dtype == GEMV_F16 ? kStateLdsOf<mbd::DT_F16>[t] : kStateLdsOf<mbd::DT_BF16>[t]; }
+size_t grad_lds(int dtype, int t) { return dtype == GEMV_F16 ? kGradLdsOf<mbd::DT_F16>[t] : kGradLdsOf<mbd::DT_BF16>[t]; }
 
 // 64, 128 or 256 channels, by index.
 int tier(int64_t d) { return d <= 64 ? 0 : d <= 128 ? 1 : 2; }
@@ -333,7 +335,7 @@ hipError_t launch_state(const gla_scan_t* p, int64_t grid, int waves, int64_t dv
   const int t = tier(dv);
   void* args[] = {(void*)&a};
   return hipLaunchKernel((const void*)(*kScanState[p->dtype])[p->gate_f32][t][waves == 4],
-                         dim3((unsigned)grid, (unsigned)sides), dim3((unsigned)waves * 64u), args, kStateLds[t], stream);
+                         dim3((unsigned)grid, (unsigned)sides), dim3((unsigned)waves * 64u), args, state_lds(p->dtype, t), stream);
 }
 
 mbd::Join join_of(const gla_scan_t* p, const ScanPlan& s, float* slots, const float* decays, const float* S0, int rev) {
@@ -356,14 +358,14 @@ bool mbd_host::scan_set_attributes() {
   const auto set = [](const void* fn, size_t lds) {
     return lds <= 65536 || hipFuncSetAttribute(fn, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds) == hipSuccess;
   };
-  static_assert(mbd::scan_state_lds<8>() <= 65536, "");
   for (int d = 0; d < 2; ++d)
     for (int g = 0; g < 2; ++g)
       for (int r = 0; r < 2; ++r)
         for (int t = 0; t < 3; ++t)
           for (int w = 0; w < 2; ++w)
             if (!set((const void*)(*kScanOut[d])[g][r][t][w], kOutLds[t]) ||
-                !set((const void*)(*kScanGrad[d])[g][r][t][w], kGradLds[t]))
+                !set((const void*)(*kScanGrad[d])[g][r][t][w], grad_lds(d, t)) ||
+                (r == 0 && !set((const void*)(*kScanState[d])[g][t][w], state_lds(d, t))))
               return false;
   return true;
 }
@@ -503,8 +505,8 @@ extern "C" gemv_status_t gla_scan_backward(gemv_handle_t h, const gla_scan_t* p,
     if (e == hipSuccess)
       e = launch_join(s, {{join_of(p, s, f.slots, f.decays, S0, 0), join_of(p, s, r.slots, r.decays, dST, 1)}}, 2, stream);
   }
-  if (e == hipSuccess) e = launch(scan_form(kScanGrad, p, 0, vt, kw == 4), gk_grid, kw, kGradLds[vt], f, stream);
-  if (e == hipSuccess) e = launch(scan_form(kScanGrad, p, 1, vt, kw == 4), gk_grid, kw, kGradLds[vt], r, stream);
+  if (e == hipSuccess) e = launch(scan_form(kScanGrad, p, 0, vt, kw == 4), gk_grid, kw, grad_lds(p->dtype, vt), f, stream);
+  if (e == hipSuccess) e = launch(scan_form(kScanGrad, p, 1, vt, kw == 4), gk_grid, kw, grad_lds(p->dtype, vt), r, stream);
   if (e == hipSuccess) e = launch(scan_form(kScanOut, p, 1, kt, ow == 4), gv_grid, ow, kOutLds[kt], o, stream);
   return e == hipSuccess ? GEMV_OK : report(h, GEMV_ERR_HIP, hipGetErrorString(e));
 }

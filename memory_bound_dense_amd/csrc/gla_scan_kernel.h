@@ -174,6 +174,13 @@ __device__ __forceinline__ void exact_terms(u32x4 raw, bf16x8 (&out)[kTerms<DT>]
   }
 }
 
+// The same for pairs: a word as one word per term.
+template <int DT>
+__device__ __forceinline__ void exact_pair(uint32_t w, uint32_t (&out)[kTerms<DT>]) {
+  if constexpr (DT == DT_F16) split2<2>(pair_lo<DT>(w), pair_hi<DT>(w), out);
+  else out[0] = w;
+}
+
 // c += a b, a of NA terms and b of NB terms (largest first): the products of
 // terms i and j with i + j < max(NA, NB); the others are below the last one kept.
 template <int NA, int NB>
@@ -792,9 +799,10 @@ __global__ __launch_bounds__(NW * 64, NS > 4 ? 1 : 2) void scan_out_kernel(const
 // with q dq left in float32 for the gates' gradient (235 MB: 2.6 TB/s), dk with
 // dg 103 us (270 MB), bound as above.
 
-template <int NV>
+template <int DT, int NV>
 constexpr size_t scan_grad_lds() {
-  return (size_t)2 * kScanC * (NV * 32 + kPadRow) * 2 + (size_t)NV * 32 * kTokRow * 2 + 6144 + 64;
+  return (size_t)(kTerms<DT> == 1 ? 2 : 4) * kScanC * (NV * 32 + kPadRow) * 2 +
+         (size_t)kTerms<DT> * NV * 32 * kTokRow * 2 + 6144 + 64;
 }
 
 template <int DT, bool G32, int NV, int NW, bool REV>
@@ -808,8 +816,10 @@ __global__ __launch_bounds__(NW * 64, NV > 4 ? 1 : 2) void scan_grad_kernel(cons
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
   uint16_t* vs = (uint16_t*)smem;               // V [32][RS]
   uint16_t* ws = vs + kScanC * RS;              // W [32][RS]
-  uint16_t* vt = ws + kScanC * RS;              // V transposed [DVP][kTokRow]
-  uint8_t* sc = (uint8_t*)(vt + DVP * kTokRow);   // the scores' terms
+  // W as terms of [32][RS]: f16 is converted once a workgroup, not by every wave
+  uint16_t* wt2 = kTerms<DT> == 1 ? ws : ws + kScanC * RS;
+  uint16_t* vt = wt2 + kTerms<DT> * kScanC * RS;   // V transposed: terms of [DVP][kTokRow]
+  uint8_t* sc = (uint8_t*)(vt + kTerms<DT> * DVP * kTokRow);   // the scores' terms
   int* wild = (int*)(sc + 6144);
 
   Place p;
@@ -900,8 +910,14 @@ __global__ __launch_bounds__(NW * 64, NV > 4 ? 1 : 2) void scan_grad_kernel(cons
       take(st, g, vw[i], v);
       u32x4 c0, c1;
       columns_of(v, c0, c1);
-      *(u32x4*)(vt + e0 * kTokRow + 8 * g) = c0;
-      *(u32x4*)(vt + (e0 + 1) * kTokRow + 8 * g) = c1;
+      bf16x8 t0[kTerms<DT>], t1[kTerms<DT>];
+      exact_terms<DT>(c0, t0);
+      exact_terms<DT>(c1, t1);
+#pragma unroll
+      for (int m = 0; m < kTerms<DT>; ++m) {
+        *(bf16x8*)(vt + (m * DVP + e0) * kTokRow + 8 * g) = t0[m];
+        *(bf16x8*)(vt + (m * DVP + e0 + 1) * kTokRow + 8 * g) = t1[m];
+      }
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         raw = pair_max(raw, v[j]);
@@ -912,6 +928,12 @@ __global__ __launch_bounds__(NW * 64, NV > 4 ? 1 : 2) void scan_grad_kernel(cons
       for (int j = 0; j < 8; ++j) {
         raw = pair_max(raw, v[j]);
         *(uint32_t*)(ws + (8 * g + j) * RS + e0) = v[j];
+        if constexpr (kTerms<DT> > 1) {
+          uint32_t t[kTerms<DT>];
+          exact_pair<DT>(v[j], t);
+#pragma unroll
+          for (int m = 0; m < kTerms<DT>; ++m) *(uint32_t*)(wt2 + (m * kScanC + 8 * g + j) * RS + e0) = t[m];
+        }
       }
       hard |= pair_wild<DT>(raw);
     }
@@ -967,13 +989,12 @@ __global__ __launch_bounds__(NW * 64, NV > 4 ? 1 : 2) void scan_grad_kernel(cons
     f32x4 pt[kMine<NW>] = {};   // this wave's W_i . V_j: rows j, columns i
 #pragma unroll
     for (int s = 0; s < NV; ++s) {
-      u32x4 wr[2];
       bf16x8 wt[2][kTerms<DT>];
 #pragma unroll
-      for (int tl = 0; tl < 2; ++tl) {
-        wr[tl] = *(const u32x4*)(ws + row_of(n, tl) * RS + 32 * s + 8 * g);
-        exact_terms<DT>(wr[tl], wt[tl]);
-      }
+      for (int tl = 0; tl < 2; ++tl)
+#pragma unroll
+        for (int m = 0; m < kTerms<DT>; ++m)
+          wt[tl][m] = *(const bf16x8*)(wt2 + (m * kScanC + row_of(n, tl)) * RS + 32 * s + 8 * g);
 #pragma unroll
       for (int m = 0; m < kMine<NW>; ++m) {
         int jt, it;
@@ -1012,7 +1033,9 @@ __global__ __launch_bounds__(NW * 64, NV > 4 ? 1 : 2) void scan_grad_kernel(cons
 #pragma unroll
       for (int tl = 0; tl < 2; ++tl) {
         bf16x8 vv[kTerms<DT>];
-        exact_terms<DT>(*(const u32x4*)(vt + (32 * s + row_of(n, tl)) * kTokRow + 8 * g), vv);
+#pragma unroll
+        for (int m = 0; m < kTerms<DT>; ++m)
+          vv[m] = *(const bf16x8*)(vt + (m * DVP + 32 * s + row_of(n, tl)) * kTokRow + 8 * g);
 #pragma unroll
         for (int nt = 0; nt < 2; ++nt) S[s][tl][nt] = mfma_terms(vv, kk[nt], S[s][tl][nt]);
       }
@@ -1165,12 +1188,14 @@ __global__ __launch_bounds__(NW * 64, NV > 4 ? 1 : 2) void scan_grad_kernel(cons
 // Where that does not hold -- factors or values beyond kBig, or factors that
 // rise again after they were tiny -- the wave does its channels over again as
 // the recurrence itself.  K and its factors stay in a wave's registers, V is
-// shared through LDS in two buffers, one barrier a chunk.  Bound by HBM: at the
-// sizes above 27 us (88 MB read, 29 MB written: 4.3 TB/s; further chunks at 5.1).
+// shared through LDS in two buffers of its terms (f16 is converted once a
+// workgroup: 73 us for 83 at 32768 tokens, 8 heads), one barrier a chunk.  Bound
+// by HBM: at the sizes above 27 us (88 MB read, 29 MB written: 4.3 TB/s; further
+// chunks at 5.1).
 
-template <int NV>
+template <int DT, int NV>
 constexpr size_t scan_state_lds() {
-  return (size_t)2 * NV * 32 * kTokRow * 2;
+  return (size_t)2 * kTerms<DT> * NV * 32 * kTokRow * 2;
 }
 constexpr float kTiny = 0x1p-110f;  // factors that get close to float32's end lose bits
 constexpr float kRise = 20.0f;      // which matter if they can rise by e^kRise (2^29) again
@@ -1215,15 +1240,21 @@ __device__ __forceinline__ void own_state(const ScanArgs& a) {
   float run[2] = {1.0f, 1.0f};          // the walked gates' decay
   float low = 1.0f, rise = 0.0f, big = 0.0f;
   for (int c = 0; c < nch; ++c) {
-    uint16_t* vt = (uint16_t*)smem + (c & 1) * DVP * kTokRow;   // V transposed [DVP][kTokRow]
+    uint16_t* vt = (uint16_t*)smem + (c & 1) * kTerms<DT> * DVP * kTokRow;   // V transposed: terms of [DVP][kTokRow]
 #pragma unroll
     for (int i = 0; i < SL; ++i) {
       const int s = wave + i * NW, e0 = 32 * s + 2 * n;
       if (NV % NW != 0 && s >= NV) break;
       u32x4 c0, c1;
       columns_of(vw[i], c0, c1);
-      *(u32x4*)(vt + e0 * kTokRow + 8 * g) = c0;
-      *(u32x4*)(vt + (e0 + 1) * kTokRow + 8 * g) = c1;
+      bf16x8 t0[kTerms<DT>], t1[kTerms<DT>];
+      exact_terms<DT>(c0, t0);
+      exact_terms<DT>(c1, t1);
+#pragma unroll
+      for (int m = 0; m < kTerms<DT>; ++m) {
+        *(bf16x8*)(vt + (m * DVP + e0) * kTokRow + 8 * g) = t0[m];
+        *(bf16x8*)(vt + (m * DVP + e0 + 1) * kTokRow + 8 * g) = t1[m];
+      }
     }
     bf16x8 kk[2][3];
     float top = 0.0f;
@@ -1266,7 +1297,9 @@ __device__ __forceinline__ void own_state(const ScanArgs& a) {
 #pragma unroll
       for (int tl = 0; tl < 2; ++tl) {
         bf16x8 vv[kTerms<DT>];
-        exact_terms<DT>(*(const u32x4*)(vt + (32 * s + row_of(n, tl)) * kTokRow + 8 * g), vv);
+#pragma unroll
+        for (int m = 0; m < kTerms<DT>; ++m)
+          vv[m] = *(const bf16x8*)(vt + (m * DVP + 32 * s + row_of(n, tl)) * kTokRow + 8 * g);
 #pragma unroll
         for (int nt = 0; nt < 2; ++nt) S[s][tl][nt] = mfma_terms(vv, kk[nt], S[s][tl][nt]);
       }
