@@ -4,6 +4,7 @@ elements, caller's scratch, and one gated-linear-attention layer run through
 all of them.  Bounds as in test_gla_scan, test_gemm and test_rmsnorm."""
 import math
 import random
+import threading
 import time
 
 import numpy as np
@@ -305,6 +306,41 @@ def test_two_streams_at_once(h):
             for i, (_, outs) in enumerate(calls):
                 for t, w in zip(outs, want[i]):
                     assert torch.equal(bits(t), w), (rep, i)
+
+
+def test_two_threads_at_once(h):
+    """Two threads with streams of their own on one handle: the bits of a quiet run."""
+    sets = [make_calls(h) for _ in range(2)]
+    want = []
+    for call, outs in sets[0]:
+        call()
+        torch.cuda.synchronize()
+        want.append([bits(t) for t in outs])
+    errors = []
+
+    def work(calls):
+        try:
+            stream = torch.cuda.Stream()
+            with torch.cuda.stream(stream):
+                for _ in range(3):
+                    for _, outs in calls:
+                        wreck(outs)
+                    for call, _ in calls:
+                        call()
+                    stream.synchronize()
+                    for (_, outs), w in zip(calls, want):
+                        for t, x in zip(outs, w):
+                            assert torch.equal(bits(t), x)
+        except BaseException as e:
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=(calls,)) for calls in sets]
+    torch.cuda.synchronize()
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors, errors[0]
 
 
 def test_callers_scratch_and_stream(scan):
