@@ -301,10 +301,11 @@ mbd::ScanTensor tensor(const gla_scan_t* p, const void* x, const gla_stride_t& s
   t.p = x;
   t.sb = p->offsets ? 0 : s.batch;
   t.sh = s.head;
-  t.st = (int32_t)s.token;
+  // one token's stride says nothing, but tells tokens behind it from it
+  t.st = (int32_t)((p->offsets ? p->rows : p->tokens) > 1 ? s.token : up(d, 2));
   // 4-byte accesses: even channels, strides and a 4-byte aligned start
   t.vec = d % 2 == 0 && (s.batch % 2 == 0 || p->offsets || p->batch == 1) && (s.head % 2 == 0 || p->heads == 1) &&
-          s.token % 2 == 0 && ((uintptr_t)x & 3u) == 0;
+          t.st % 2 == 0 && ((uintptr_t)x & 3u) == 0;
   return t;
 }
 

@@ -95,6 +95,26 @@ def test_layouts_give_the_same_bits(scan, t, dk, dv, layout):
         assert (full == fill).all(), n
 
 
+@pytest.mark.parametrize("stride", [0, 1, 7])
+@pytest.mark.parametrize("packed", [False, True])
+def test_one_token_of_any_stride(scan, stride, packed):
+    """The token stride of a single token is never used: the bits of a dense tensor."""
+    x = tg.cuda(tg.inputs(1, 1, 3, 64, 40, BF, F32, seed=2))
+    off = torch.tensor([0, 1], dtype=torch.int32, device="cuda") if packed else None
+    got = []
+    for st in (None, stride):
+        like = lambda t: t if st is None else torch.as_strided(t, t.shape, (t.stride(0), st, t.stride(2), 1))
+        o, ST, dS0 = torch.empty_like(x["v"]), torch.empty_like(x["S0"]), torch.empty_like(x["S0"])
+        r = [torch.empty_like(x[n]) for n in ("q", "k", "v", "g")]
+        y = [like(x[n]) for n in NAMES]
+        scan.forward(*y[:4], like(o), x["scale"], S0=x["S0"], ST=ST, offsets=off)
+        scan.backward(*y, *[like(t) for t in r], x["scale"], S0=x["S0"], dST=x["dST"], dS0=dS0, offsets=off)
+        torch.cuda.synchronize()
+        got.append([o, ST, dS0] + r)
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
+
+
 def test_broadcast_inputs(scan):
     """k, v and the gates shared by all heads (stride 0): the results of expanded copies."""
     b, t, h, dk, dv = 2, 70, 4, 64, 64
