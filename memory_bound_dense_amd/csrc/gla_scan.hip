@@ -296,7 +296,8 @@ size_t grad_lds(int dtype, int t) { return dtype == GEMV_F16 ? kGradLdsOf<mbd::D
 // 64, 128 or 256 channels, by index.
 int tier(int64_t d) { return d <= 64 ? 0 : d <= 128 ? 1 : 2; }
 
-mbd::ScanTensor tensor(const gla_scan_t* p, const void* x, const gla_stride_t& s, int64_t d) {
+int gate_bytes(const gla_scan_t* p) { return p->gate_f32 ? 4 : 2; }
+mbd::ScanTensor tensor(const gla_scan_t* p, const void* x, const gla_stride_t& s, int64_t d, int bytes = 2) {
   mbd::ScanTensor t;
   t.p = x;
   t.sb = p->offsets ? 0 : s.batch;
@@ -306,6 +307,8 @@ mbd::ScanTensor tensor(const gla_scan_t* p, const void* x, const gla_stride_t& s
   // 4-byte accesses: even channels, strides and a 4-byte aligned start
   t.vec = d % 2 == 0 && (s.batch % 2 == 0 || p->offsets || p->batch == 1) && (s.head % 2 == 0 || p->heads == 1) &&
           t.st % 2 == 0 && ((uintptr_t)x & 3u) == 0;
+  t.step = (uint32_t)t.st * (uint32_t)bytes;
+  t.full = (uint32_t)((mbd::kScanC - 1) * (uint64_t)t.step + (uint64_t)d * bytes);   // < 2^31
   return t;
 }
 
@@ -408,7 +411,7 @@ extern "C" gemv_status_t gla_scan_forward(gemv_handle_t h, const gla_scan_t* p, 
   mbd::ScanArgs a = common(p, s);
   a.K = tensor(p, k, p->k, p->dk);
   a.V = tensor(p, v, p->v, p->dv);
-  a.G = tensor(p, gk, p->gk, p->dk);
+  a.G = tensor(p, gk, p->gk, p->dk, gate_bytes(p));
   a.X = tensor(p, q, p->q, p->dk);
   a.O = tensor(p, o, p->o, p->dv);
   a.kscale = 1.0f;
@@ -458,7 +461,7 @@ extern "C" gemv_status_t gla_scan_backward(gemv_handle_t h, const gla_scan_t* p,
   const ScanPlan s = scan_plan(p, true);
   char* w = (char*)workspace;
   const mbd::ScanTensor tq = tensor(p, q, p->q, p->dk), tk = tensor(p, k, p->k, p->dk),
-                        tv = tensor(p, v, p->v, p->dv), tg = tensor(p, gk, p->gk, p->dk),
+                        tv = tensor(p, v, p->v, p->dv), tg = tensor(p, gk, p->gk, p->dk, gate_bytes(p)),
                         tdo = tensor(p, dout, p->o, p->dv);
   const int kw = waves_of(p->dk), cols = out_cols(p->dv), ow = waves_of(cols);
   const int kt = tier(p->dk), vt = tier(p->dv);
@@ -481,7 +484,7 @@ extern "C" gemv_status_t gla_scan_backward(gemv_handle_t h, const gla_scan_t* p,
   r.W = tv;
   r.X = tk;
   r.O = tensor(p, dk, grad->dk, p->dk);
-  r.DG = tensor(p, dgk, grad->dgk, p->dk);
+  r.DG = tensor(p, dgk, grad->dgk, p->dk, gate_bytes(p));
   r.kscale = p->scale;
   r.oscale = 1.0f;
   r.S0 = dST;

@@ -67,6 +67,8 @@ struct ScanTensor {
   int64_t sb, sh;
   int32_t st;     // <= 2^24
   int32_t vec;    // channel pairs may be moved as one access
+  uint32_t step;  // bytes of a token's stride
+  uint32_t full;  // bytes from a chunk's first to behind its last element
 };
 
 struct ScanArgs {
@@ -214,20 +216,18 @@ __device__ __forceinline__ Lane lane_of(const ScanTensor& x, int g, int c0, int 
   Lane l;
   l.off0 = c0 < width ? (row + (uint32_t)c0) * bytes : kOffsetOutOfRange;
   l.lone = c0 + 1 == width;
-  l.step = (uint32_t)x.st * bytes;
+  l.step = x.step;
   return l;
 }
-// The n valid tokens at `at` (none: an empty range).
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t chunk_rsrc(const ScanTensor& x, const char* at, int n, int width,
-                                                             int bytes) {
-  const uint32_t len = n > 0 ? ((uint32_t)(n - 1) * (uint32_t)x.st + (uint32_t)width) * bytes : 0u;
-  return make_rsrc(at, len);
+// The first n (at least 1) of the 32 tokens at `at`.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t chunk_rsrc(const ScanTensor& x, const char* at, int n) {
+  return make_rsrc(at, x.full - (uint32_t)(kScanC - n) * x.step);
 }
 // To the next chunk in the order of the recurrence.
 template <bool REV>
-__device__ __forceinline__ void walk(const ScanTensor& x, const char*& at, int bytes) {
-  const int64_t by = (int64_t)(kScanC * bytes) * x.st;
-  at += REV ? -by : by;
+__device__ __forceinline__ void walk(const ScanTensor& x, const char*& at) {
+  const uint64_t by = (uint64_t)x.step * kScanC;
+  at = REV ? at - by : at + by;
 }
 // The lane's offsets as the loop's own values: the 8 tokens' offsets are then
 // formed where they are used, not kept in 8 registers per tensor over the loop.
@@ -585,19 +585,19 @@ __global__ __launch_bounds__(NW * 64, NS > 4 ? 1 : 2) void scan_out_kernel(const
   auto fetch = [&](int c) {
     const int64_t tok = p.lo + (int64_t)(REV ? nch - 1 - c : c) * kScanC;
     const int nv = (int)min((int64_t)kScanC, p.hi - tok);
-    const auto gr = chunk_rsrc(a.G, gbp, nv, a.dk, gb), kr = chunk_rsrc(a.K, kb, nv, a.dk, 2),
-               xr = chunk_rsrc(a.X, xb, nv, a.dk, 2);
+    const auto gr = chunk_rsrc(a.G, gbp, nv), kr = chunk_rsrc(a.K, kb, nv),
+               xr = chunk_rsrc(a.X, xb, nv);
 #pragma unroll
     for (int i = 0; i < SL; ++i) {
       load_gates<REV, G32>(gr, gl[i], a.G.vec, gw[i]);
       load16<REV>(kr, kl[i], a.K.vec, kw[i]);
       load16<REV>(xr, xl[i], a.X.vec, xw[i]);
     }
-    load16<REV>(chunk_rsrc(a.V, vb, nv, a.dv, 2), vl, a.V.vec, vw);
-    walk<REV>(a.G, gbp, gb);
-    walk<REV>(a.K, kb, 2);
-    walk<REV>(a.X, xb, 2);
-    walk<REV>(a.V, vb, 2);
+    load16<REV>(chunk_rsrc(a.V, vb, nv), vl, a.V.vec, vw);
+    walk<REV>(a.G, gbp);
+    walk<REV>(a.K, kb);
+    walk<REV>(a.X, xb);
+    walk<REV>(a.V, vb);
   };
   if (nch > 0) fetch(0);
   // a step's second half e^{end-r} is left to the next step, which scales the
@@ -755,14 +755,14 @@ __global__ __launch_bounds__(NW * 64, NS > 4 ? 1 : 2) void scan_out_kernel(const
 #pragma unroll
       for (int nt = 0; nt < 2; ++nt) o[it][nt] = mfma_terms(ps, vt[nt], o[it][nt]);
     }
-    const __amdgpu_buffer_rsrc_t orsrc = chunk_rsrc(a.O, ob, nv, a.dv, 2);
+    const __amdgpu_buffer_rsrc_t orsrc = chunk_rsrc(a.O, ob, nv);
     const Lane ot = fresh(ol);
 #pragma unroll
     for (int j = 0; j < 8; ++j)
       if (now.width == 32 || takes(now, g, j))
         store16<REV>(orsrc, ot, a.O.vec, j,
                      pair_round<DT>(o[j >> 2][0][j & 3] * a.oscale, o[j >> 2][1][j & 3] * a.oscale));
-    if (next != c) walk<REV>(a.O, ob, 2);
+    if (next != c) walk<REV>(a.O, ob);
     c = next;
   }
 
@@ -795,9 +795,9 @@ __global__ __launch_bounds__(NW * 64, NS > 4 ? 1 : 2) void scan_out_kernel(const
 // A wave owns 32 channels (columns of the transposed state, 64 VGPRs at DV
 // 128) and their part of the output; K e^{r-G} of its channels never leaves
 // its registers.  V and W go through LDS, row-major for the products over DV
-// and V also transposed for the state's update.  At the sizes above: dq 90 us
+// and V also transposed for the state's update.  At the sizes above: dq 89 us
 // with q dq left in float32 for the gates' gradient (235 MB: 2.6 TB/s), dk with
-// dg 103 us (270 MB), bound as above.
+// dg 102 us (270 MB), bound as above.
 
 template <int DT, int NV>
 constexpr size_t scan_grad_lds() {
@@ -881,18 +881,18 @@ __global__ __launch_bounds__(NW * 64, NV > 4 ? 1 : 2) void scan_grad_kernel(cons
   auto fetch = [&](int c) {
     const int64_t tok = p.lo + (int64_t)(REV ? nch - 1 - c : c) * kScanC;
     const int nv = (int)min((int64_t)kScanC, p.hi - tok);
-    const auto vr = chunk_rsrc(a.V, vb, nv, a.dv, 2);
+    const auto vr = chunk_rsrc(a.V, vb, nv);
 #pragma unroll
     for (int i = 0; i < SL; ++i) load16<REV>(vr, vl[i], a.V.vec, vw[i]);
-    const auto wr = chunk_rsrc(a.W, wb, nv, a.dv, 2);
+    const auto wr = chunk_rsrc(a.W, wb, nv);
 #pragma unroll
     for (int i = 0; i < SL; ++i) load16<REV>(wr, wl[i], a.W.vec, ww[i]);
-    walk<REV>(a.W, wb, 2);
-    load_gates<REV, G32>(chunk_rsrc(a.G, gbp, nv, a.dk, gb), gl, a.G.vec, gw);
-    load16<REV>(chunk_rsrc(a.K, kb, nv, a.dk, 2), kl, a.K.vec, kw);
-    walk<REV>(a.V, vb, 2);
-    walk<REV>(a.G, gbp, gb);
-    walk<REV>(a.K, kb, 2);
+    walk<REV>(a.W, wb);
+    load_gates<REV, G32>(chunk_rsrc(a.G, gbp, nv), gl, a.G.vec, gw);
+    load16<REV>(chunk_rsrc(a.K, kb, nv), kl, a.K.vec, kw);
+    walk<REV>(a.V, vb);
+    walk<REV>(a.G, gbp);
+    walk<REV>(a.K, kb);
   };
   if (nch > 0) fetch(0);
   if (!REV) load_state();
@@ -977,7 +977,7 @@ __global__ __launch_bounds__(NW * 64, NV > 4 ? 1 : 2) void scan_grad_kernel(cons
       left[nt] = q.b[nt];
     }
     uint32_t xw[8];
-    load16<REV>(chunk_rsrc(a.X, xb, nv, a.dk, 2), xl, a.X.vec, xw);
+    load16<REV>(chunk_rsrc(a.X, xb, nv), xl, a.X.vec, xw);
     const Step now = st;
     advance(st);
     const int next = st.pos == kScanC ? c + 1 : c;
@@ -1056,7 +1056,7 @@ __global__ __launch_bounds__(NW * 64, NV > 4 ? 1 : 2) void scan_grad_kernel(cons
         }
       }
     }
-    const __amdgpu_buffer_rsrc_t orsrc = chunk_rsrc(a.O, ob, nv, a.dk, 2);
+    const __amdgpu_buffer_rsrc_t orsrc = chunk_rsrc(a.O, ob, nv);
     const Lane ot = fresh(ol);
     float y[2][8];
 #pragma unroll
@@ -1091,7 +1091,7 @@ __global__ __launch_bounds__(NW * 64, NV > 4 ? 1 : 2) void scan_grad_kernel(cons
           d[nt][j] = run[nt];
         }
       }
-      const __amdgpu_buffer_rsrc_t drsrc = chunk_rsrc(a.DG, dgb, nv, a.dk, gb);
+      const __amdgpu_buffer_rsrc_t drsrc = chunk_rsrc(a.DG, dgb, nv);
       const Lane dt = fresh(dl);
 #pragma unroll
       for (int nt = 0; nt < 2; ++nt) {
@@ -1120,9 +1120,9 @@ __global__ __launch_bounds__(NW * 64, NV > 4 ? 1 : 2) void scan_grad_kernel(cons
       }
     }
     if (next != c) {
-      walk<REV>(a.X, xb, 2);
-      walk<REV>(a.O, ob, 2);
-      if (REV) walk<REV>(a.DG, dgb, gb);
+      walk<REV>(a.X, xb);
+      walk<REV>(a.O, ob);
+      if (REV) walk<REV>(a.DG, dgb);
     }
     c = next;
   }
@@ -1226,14 +1226,14 @@ __device__ __forceinline__ void own_state(const ScanArgs& a) {
   auto fetch = [&](int c) {
     const int64_t tok = p.lo + (int64_t)(DIR ? nch - 1 - c : c) * kScanC;
     const int nv = (int)min((int64_t)kScanC, p.hi - tok);
-    const auto vr = chunk_rsrc(a.V, vb, nv, a.dv, 2);
+    const auto vr = chunk_rsrc(a.V, vb, nv);
 #pragma unroll
     for (int i = 0; i < SL; ++i) load16<DIR>(vr, vl[i], a.V.vec, vw[i]);
-    load_gates<DIR, G32>(chunk_rsrc(a.G, gbp, nv, a.dk, gb), gl, a.G.vec, gw);
-    load16<DIR>(chunk_rsrc(a.K, kb, nv, a.dk, 2), kl, a.K.vec, kw);
-    walk<DIR>(a.V, vb, 2);
-    walk<DIR>(a.G, gbp, gb);
-    walk<DIR>(a.K, kb, 2);
+    load_gates<DIR, G32>(chunk_rsrc(a.G, gbp, nv), gl, a.G.vec, gw);
+    load16<DIR>(chunk_rsrc(a.K, kb, nv), kl, a.K.vec, kw);
+    walk<DIR>(a.V, vb);
+    walk<DIR>(a.G, gbp);
+    walk<DIR>(a.K, kb);
   };
   if (nch > 0) fetch(0);
   f32x4 S[NV][2][2] = {};               // rows: DV, columns: the lane's channels
