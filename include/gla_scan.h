@@ -25,7 +25,7 @@
  * Layout: element strides per tensor, so (batch, token, head, channel) and
  * (batch, head, token, channel) tensors and slices of fused projections are
  * taken as they are; channels are dense.  Token strides are 0 < stride <=
- * 2^24 elements and at least the channels (with more than one token); an
+ * 2^24 elements and at least the channels (a single token's is not used); an
  * input's batch and head strides may be 0 (a broadcast input: its gradient is
  * returned per head, unsummed).  An output's elements must not overlap each
  * other, another output or an input; the exception is ST == S0 (the state

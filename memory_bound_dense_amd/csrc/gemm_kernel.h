@@ -721,6 +721,7 @@ __global__ __launch_bounds__(WN * WM * WK * 64, 2) void gemm_direct_kernel(const
 }
 
 // The splits' sums added in order, then the epilogue: one thread per 4 outputs.
+// 101 x 18433 outputs of 3 splits, with bias, gelu and residual: 11 us (30 MB).
 static __global__ __launch_bounds__(256) void gemm_join_kernel(const GemmArgs p) {
   const int64_t e = ((int64_t)blockIdx.x * 256 + threadIdx.x);
   const int per = p.npad / 4;
