@@ -17,10 +17,11 @@
  * are float32, dense (sequence, head, dk, dv), the layout of gla_decode_step.
  * States and all sums are held in float32; each 16-bit output is rounded once,
  * to nearest-even.  Any gate is taken: one of -inf clears the state, positive
- * ones let it grow.  A value that is not finite reaches the outputs that
- * depend on it and no earlier token's (o) or later token's (gradients of k
- * and v); a state that holds one makes every output that reads its row NaN or
- * infinite.
+ * ones let it grow; a token's exp(gk) is a float32 (0 below -104, infinite
+ * above 88.7), as in gla_decode_step, the decay over many tokens is not.  A
+ * value that is not finite reaches the outputs that depend on it and no earlier
+ * token's (o) or later token's (gradients of k and v); a state that holds one
+ * makes every output that reads its row NaN or infinite.
  *
  * Layout: element strides per tensor, so (batch, token, head, channel) and
  * (batch, head, token, channel) tensors and slices of fused projections are

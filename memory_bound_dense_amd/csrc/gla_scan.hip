@@ -18,7 +18,7 @@ namespace mbd {
 // 4 segments fetched at once).
 struct Join {
   float* slots;
-  const float* decays;
+  const Decay* decays;
   const float* S0;          // user layout, or null
   const int32_t* offsets;
   int64_t total, t;
@@ -49,11 +49,11 @@ __global__ __launch_bounds__(256) void scan_join_kernel(const JoinArgs both) {
   }
   const int64_t size = (int64_t)a.dkp * a.dvp;
   float* slot = a.slots + head * a.nseg * size + (int64_t)d * a.dvp + e;
-  const float* decay = a.decays + head * a.nseg * a.dkp + d;
+  const Decay* decay = a.decays + head * a.nseg * a.dkp + d;
   constexpr int AHEAD = 8;   // segments fetched at once
   for (int s0 = 0; s0 + 1 < ns; s0 += AHEAD) {
     f32x4 u[AHEAD];
-    float f[AHEAD];
+    Decay f[AHEAD];
 #pragma unroll
     for (int m = 0; m < AHEAD; ++m)
       if (s0 + m + 1 < ns) {
@@ -66,9 +66,8 @@ __global__ __launch_bounds__(256) void scan_join_kernel(const JoinArgs both) {
       if (s0 + m + 1 < ns) {
         const int64_t at = a.rev ? ns - 1 - s0 - m : s0 + m;
         *(f32x4*)(slot + at * size) = x;
-        // a state of zeros stays one, also where the segment's decay is beyond float32
 #pragma unroll
-        for (int r = 0; r < 4; ++r) x[r] = x[r] == 0.0f && f[m] > 3e38f ? u[m][r] : __builtin_fmaf(x[r], f[m], u[m][r]);
+        for (int r = 0; r < 4; ++r) x[r] = scaled(x[r], f[m]) + u[m][r];
       }
   }
   *(f32x4*)(slot + (a.rev ? 0 : ns - 1) * size) = x;
@@ -142,10 +141,10 @@ ScanPlan scan_plan(const gla_scan_t* p, bool backward) {
   const size_t states = (size_t)s.heads * s.nseg * s.dkp * s.dvp * 4, chans = (size_t)s.heads * s.nseg * s.dkp * 4;
   if (s.nseg > 1) {
     s.slots = take(states);
-    s.decays = take(chans);
+    s.decays = take(chans / sizeof(float) * sizeof(mbd::Decay));
     if (backward) {
       s.slots2 = take(states);
-      s.decays2 = take(chans);
+      s.decays2 = take(chans / sizeof(float) * sizeof(mbd::Decay));
     }
   }
   if (backward) {
@@ -342,7 +341,7 @@ hipError_t launch_state(const gla_scan_t* p, int64_t grid, int waves, int64_t dv
                          dim3((unsigned)grid, (unsigned)sides), dim3((unsigned)waves * 64u), args, state_lds(p->dtype, t), stream);
 }
 
-mbd::Join join_of(const gla_scan_t* p, const ScanPlan& s, float* slots, const float* decays, const float* S0, int rev) {
+mbd::Join join_of(const gla_scan_t* p, const ScanPlan& s, float* slots, const mbd::Decay* decays, const float* S0, int rev) {
   return mbd::Join{slots, decays, S0, p->offsets, p->rows, p->tokens, (int32_t)p->heads, (int32_t)p->dk,
                    (int32_t)p->dv, s.dkp, s.dvp, s.nseg, s.L, rev};
 }
@@ -426,7 +425,7 @@ extern "C" gemv_status_t gla_scan_forward(gemv_handle_t h, const gla_scan_t* p, 
   if (s.nseg > 1) {
     char* w = (char*)workspace;
     a.slots = (float*)(w + s.slots);
-    a.decays = (float*)(w + s.decays);
+    a.decays = (mbd::Decay*)(w + s.decays);
     // a segment's own state: columns in blocks of at most 256, channels in blocks of a workgroup's
     mbd::StateArgs sides = {a, {}};
     mbd::ScanArgs& b = sides.fwd;
@@ -501,9 +500,9 @@ extern "C" gemv_status_t gla_scan_backward(gemv_handle_t h, const gla_scan_t* p,
   hipError_t e = hipSuccess;
   if (s.nseg > 1) {
     f.slots = (float*)(w + s.slots);
-    f.decays = (float*)(w + s.decays);
+    f.decays = (mbd::Decay*)(w + s.decays);
     r.slots = o.slots = (float*)(w + s.slots2);
-    r.decays = o.decays = (float*)(w + s.decays2);
+    r.decays = o.decays = (mbd::Decay*)(w + s.decays2);
     f.others = r.slots;
     e = launch_state(p, gk_grid, kw, p->dv, {f, r}, 2, stream);
     if (e == hipSuccess)

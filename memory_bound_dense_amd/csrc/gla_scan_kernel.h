@@ -71,6 +71,14 @@ struct ScanTensor {
   uint32_t full;  // bytes from a chunk's first to behind its last element
 };
 
+// A factor m 2^e, m in [0.5, 1) (or 0, infinite or NaN): a segment's decay may be
+// far beyond float32 in either direction and its product with a state still be in
+// range (128 gates of 0.9 over 1e-15, -120 and then 120 over 1e25).
+struct Decay {
+  float m;
+  int32_t e;
+};
+
 struct ScanArgs {
   ScanTensor K, V, G;      // the state's own inputs
   ScanTensor X;            // out: the side multiplied with the state; grad: q (forward) or k
@@ -82,7 +90,7 @@ struct ScanArgs {
   const float* S0;         // state before the first chunk (user layout), or null: zeros
   float* ST;               // state after the last chunk (user layout), or null
   float* slots;            // per segment: its start state, [dkp][dvp]; null: one segment
-  float* decays;           // state-only: a segment's whole decay, [dkp]
+  Decay* decays;           // state-only: a segment's whole decay, [dkp]
   const float* others;     // grad, forward: the slots of the reversed recurrence, or null
   const float* dST;        // grad, forward: dS_T or null
   float* ends;             // grad: rowsum(S D) at the end of each segment, [dkp]
@@ -437,6 +445,21 @@ __device__ __forceinline__ void take(const Step& t, int g, const uint32_t (&from
       if (!takes(t, g, j)) to[j] = 0u;
   }
 }
+// d times f.
+__device__ __forceinline__ void times(Decay& d, float f) {
+  const float m = d.m * f;
+  d.m = __builtin_amdgcn_frexp_mantf(m);
+  d.e = min(max(d.e + __builtin_amdgcn_frexp_expf(m), -(1 << 28)), 1 << 28);
+}
+__device__ __forceinline__ void times(Decay& d, Decay f) {
+  d.e = min(max(d.e + f.e, -(1 << 28)), 1 << 28);
+  times(d, f.m);
+}
+// x times d.
+__device__ __forceinline__ float scaled(float x, Decay d) {
+  return d.e > 0 && d.m > 0.0f ? ldexpf(x, d.e - 1) * (2.0f * d.m) : ldexpf(x * d.m, d.e);
+}
+
 // Gates of a step: of the chunk, of 8 tokens (the others' are 0), or of one
 // token, whose decay acts as a whole before it (forward) or after it (reversed)
 // and needs no pair of factors -- so it may be 0, infinite or NaN.
@@ -1185,9 +1208,11 @@ __global__ __launch_bounds__(NW * 64, NV > 4 ? 1 : 2) void scan_grad_kernel(cons
 // the recurrence, so a token's factor is the running product of what has been
 // walked and the sums are never rescaled: no chunk is cut for its gates' sake,
 // and a factor that underflows belongs to a contribution that has decayed.
-// Where that does not hold -- factors or values beyond kBig, or factors that
-// rise again after they were tiny -- the wave does its channels over again as
-// the recurrence itself.  K and its factors stay in a wave's registers, V is
+// Where that does not hold -- factors or values beyond kBig, factors that
+// rise again after they were tiny, 8 gates whose product is not a normal number
+// -- the wave does its channels over again as the recurrence itself.  The
+// segment's whole decay, for the state at its start, is kept with an exponent of
+// its own.  K and its factors stay in a wave's registers, V is
 // shared through LDS in two buffers of its terms (f16 is converted once a
 // workgroup: 73 us for 83 at 32768 tokens, 8 heads), one barrier a chunk.  Bound
 // by HBM: at the sizes above 27 us (88 MB read, 29 MB written: 4.3 TB/s; further
@@ -1239,6 +1264,7 @@ __device__ __forceinline__ void own_state(const ScanArgs& a) {
   f32x4 S[NV][2][2] = {};               // rows: DV, columns: the lane's channels
   float run[2] = {1.0f, 1.0f};          // the walked gates' decay
   float low = 1.0f, rise = 0.0f, big = 0.0f;
+  Decay whole[2] = {{0.5f, 1}, {0.5f, 1}};   // of the lane's tokens
   for (int c = 0; c < nch; ++c) {
     uint16_t* vt = (uint16_t*)smem + (c & 1) * kTerms<DT> * DVP * kTokRow;   // V transposed: terms of [DVP][kTokRow]
 #pragma unroll
@@ -1260,16 +1286,20 @@ __device__ __forceinline__ void own_state(const ScanArgs& a) {
     float top = 0.0f;
 #pragma unroll
     for (int ch = 0; ch < 2; ++ch) {
-      float P[8], of = 1.0f;
+      float P[8], of = 1.0f, bottom = 0.0f;
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const float x = gate_value<DT, G32>(gw, ch, j);
         top = __builtin_fmaxf(top, x);
+        bottom = __builtin_fminf(bottom, x);
         const float e = __builtin_amdgcn_exp2f(x * 1.44269504f);
         if (DIR) P[j] = of;
         of = j == 0 ? e : of * e;
         if (!DIR) P[j] = of;
       }
+      times(whole[ch], of);
+      // a gate of -104 is a factor of 0 in float32
+      if (of < 0x1p-120f && bottom > -104.0f) big = __builtin_inff();
       // times the groups walked before this one, and the chunks before
       const float next = __shfl_xor(of, 16, 64), both = of * next;
       const float other = __shfl_xor(both, 32, 64);
@@ -1309,9 +1339,13 @@ __device__ __forceinline__ void own_state(const ScanArgs& a) {
   rise += __shfl_xor(rise, 32, 64);
   low = __builtin_fminf(low, __shfl_xor(low, 16, 64));
   low = __builtin_fminf(low, __shfl_xor(low, 32, 64));
+#pragma unroll
+  for (int ch = 0; ch < 2; ++ch)
+#pragma unroll
+    for (int x = 16; x <= 32; x *= 2) times(whole[ch], Decay{__shfl_xor(whole[ch].m, x, 64), __shfl_xor(whole[ch].e, x, 64)});
   if (__ballot(!(big <= kBig) || (rise > kRise && low < kTiny))) {
     const char *k1 = (const char*)a.K.p, *v1 = (const char*)a.V.p, *g1 = (const char*)a.G.p;
-    run[0] = run[1] = 1.0f;
+    whole[0] = whole[1] = Decay{0.5f, 1};
 #pragma unroll
     for (int s = 0; s < NV; ++s)
 #pragma unroll
@@ -1330,7 +1364,7 @@ __device__ __forceinline__ void own_state(const ScanArgs& a) {
           k[nt] = widen<DT>(kr[col + nt]) * (REV ? a.kscale : 1.0f);
           ex[nt] = expf(G32 ? ((const float*)gr)[col + nt] : widen<DT>(((const uint16_t*)gr)[col + nt]));
         }
-        run[nt] *= ex[nt];
+        times(whole[nt], ex[nt]);
       }
 #pragma unroll
       for (int s = 0; s < NV; ++s)
@@ -1363,7 +1397,7 @@ __device__ __forceinline__ void own_state(const ScanArgs& a) {
   if (g == 0)
 #pragma unroll
     for (int nt = 0; nt < 2; ++nt)
-      if (col + nt < a.dkp) a.decays[p.slot * a.dkp + col + nt] = run[nt];
+      if (col + nt < a.dkp) a.decays[p.slot * a.dkp + col + nt] = whole[nt];
 }
 
 // The two recurrences of a backward pass side by side (grid y), or the forward one alone.

@@ -1,0 +1,67 @@
+"""GPU: the GLA scan where decays, states or values are far apart in size,
+within the bounds of scan_bounds."""
+import pytest
+import torch
+
+import test_gla_scan as tg
+from test_gla_scan import scan  # noqa: F401 (fixture)
+from test_scan_bounds import check
+
+pytestmark = pytest.mark.gpu
+BF, HF, F32 = torch.bfloat16, torch.float16, torch.float32
+
+
+def run(scan, x, heads):  # noqa: F811
+    """The calls for `heads` heads of the data of x's one (head stride 0): the first head's results,
+    which all others have to equal."""
+    t, dk, dv = x["q"].shape[1], x["q"].shape[3], x["v"].shape[3]
+    d = tg.cuda(x)
+    for n in ("q", "k", "v", "g", "do"):
+        d[n] = d[n].expand(1, t, heads, -1)
+    for n in ("S0", "dST"):
+        if d[n] is not None:
+            d[n] = d[n].expand(1, heads, dk, dv).contiguous()
+    full = lambda dt, *s: torch.full(s, float("nan"), dtype=dt, device="cuda")
+    dt = x["q"].dtype
+    o, ST = full(dt, 1, t, heads, dv), full(F32, 1, heads, dk, dv)
+    scan.forward(d["q"], d["k"], d["v"], d["g"], o, x["scale"], S0=d["S0"], ST=ST)
+    r = {n: full(x["g"].dtype if n == "dg" else dt, 1, t, heads, w)
+         for n, w in (("dq", dk), ("dk", dk), ("dv", dv), ("dg", dk))}
+    r["dS0"] = full(F32, 1, heads, dk, dv)
+    scan.backward(d["q"], d["k"], d["v"], d["g"], d["do"], r["dq"], r["dk"], r["dv"], r["dg"], x["scale"],
+                  S0=d["S0"], dST=d["dST"], dS0=r["dS0"])
+    torch.cuda.synchronize()
+    for y in (o, r["dq"], r["dk"], r["dv"], r["dg"]):
+        assert torch.equal(y.nan_to_num(7.0), y[:, :, :1].expand_as(y).nan_to_num(7.0))
+    return o[:, :, :1], ST[:, :1], {n: y[:, :, :1] if n != "dS0" else y[:, :1] for n, y in r.items()}
+
+
+def alone(x, S0, dST):
+    """Without keys and output gradients: the start state and dST are all there is, of the given sizes."""
+    x["k"][:] = 0
+    x["do"][:] = 0
+    x["S0"] *= S0
+    x["dST"] *= dST
+    return x
+
+
+@pytest.mark.parametrize("heads", [4, 256, 1024])
+@pytest.mark.parametrize("kind", ["grow", "dip", "deep"])
+@pytest.mark.parametrize("gt", [BF, F32], ids=["bf16", "f32gate"])
+def test_decays_of_a_segment_beyond_float32(scan, kind, gt, heads):  # noqa: F811
+    """Segments of 32 (4 heads) and 256 (256 heads) tokens and whole sequences (1024): a state that
+    is in range all the way comes out the same, though its decay over a segment is e^115, or e^-120
+    on the way to 1, or 8 neighbouring gates' e^-96."""
+    x = tg.inputs(1, 1024, 1, 32, 32, BF, gt)
+    x["g"][:] = 0
+    if kind == "grow":
+        x["g"][:, 300:428] = 0.9
+        alone(x, 1e-15, 1e-30)
+    elif kind == "dip":
+        x["g"][:, 300:400] = -1.2
+        x["g"][:, 400:500] = 1.2
+        alone(x, 1e25, 1e-20)
+    else:
+        x["g"][:, 300:308] = -12.0
+        alone(x, 1e30, 1e30)
+    check(x, *run(scan, x, heads))
