@@ -422,18 +422,35 @@ constexpr int kPadRow = 8;              // 16-bit elements behind each row of a 
 constexpr int kTokRow = kScanC + 8;     // tokens per row of a transposed tile, padded
 
 // The tokens [pos, pos + width) that a step takes: the whole chunk (32), or, where
-// the gates or values do not allow it, 8 (those of one lane group) or 1.
+// the gates or values do not allow it, 8 (those of one lane group) or 1.  A step
+// scales the state by its own first half's decay and what the step before left, in
+// one product; of a token's decay, which may be anything, that product could leave
+// float32's range where the state does not.  So a step of no tokens (its `then`
+// is the width behind it) lies between steps of one token, whose decay is the first
+// half forward and what is left reversed, and those with another half of theirs there.
 struct Step {
-  int pos, width;
+  int pos, width, then;
 };
 __device__ __forceinline__ bool takes(const Step& t, int g, int j) {
   return (uint32_t)(8 * g + j - t.pos) < (uint32_t)t.width;
 }
-// What a step that was refused is tried with, and the step after `t`.
-__device__ __forceinline__ void smaller(Step& t) { t.width = t.width == 32 ? 8 : 1; }
+// What a step that was refused is tried with, the step after `t`, and the next
+// chunk's first one.
+template <bool REV>
+__device__ __forceinline__ void smaller(Step& t) {
+  if (t.width == 32) t.width = 8;
+  else if (REV) t.width = 1;
+  else t = Step{t.pos, 0, 1};
+}
+template <bool REV>
 __device__ __forceinline__ void advance(Step& t) {
   t.pos += t.width;
-  if ((t.pos & 7) == 0 && t.width == 1) t.width = 8;
+  if (t.width == 0) t.width = t.then;
+  else if ((t.pos & 7) == 0 && t.width == 1) t = REV ? Step{t.pos, 0, 8} : Step{t.pos, 8, 0};
+}
+template <bool REV>
+__device__ __forceinline__ Step first_step(const Step& before) {
+  return REV && before.width == 1 ? Step{0, 0, 32} : Step{0, 32, 0};
 }
 // The words of the step's tokens; others read as 0.
 __device__ __forceinline__ void take(const Step& t, int g, const uint32_t (&from)[8], uint32_t (&to)[8]) {
@@ -460,7 +477,7 @@ __device__ __forceinline__ float scaled(float x, Decay d) {
   return d.e > 0 && d.m > 0.0f ? ldexpf(x, d.e - 1) * (2.0f * d.m) : ldexpf(x * d.m, d.e);
 }
 
-// Gates of a step: of the chunk, of 8 tokens (the others' are 0), or of one
+// Gates of a step: of the chunk, of 8 tokens or none (the others' are 0), or of one
 // token, whose decay acts as a whole before it (forward) or after it (reversed)
 // and needs no pair of factors -- so it may be 0, infinite or NaN.
 template <int DT, bool G32, bool REV>
@@ -485,7 +502,7 @@ __device__ __forceinline__ void step_gates(const Step& t, const uint32_t (&gw)[k
   uint32_t w[kGateWords<G32>];
 #pragma unroll
   for (int j = 0; j < kGateWords<G32>; ++j) w[j] = gw[j];
-  if (t.width == 8 && g != t.pos >> 3) {
+  if (t.width < 32 && (t.width == 0 || g != t.pos >> 3)) {
 #pragma unroll
     for (int j = 0; j < kGateWords<G32>; ++j) w[j] = 0u;
   }
@@ -628,7 +645,7 @@ __global__ __launch_bounds__(NW * 64, NS > 4 ? 1 : 2) void scan_out_kernel(const
   float left[SL][2], half[SL][2];
 #pragma unroll
   for (int i = 0; i < SL; ++i) left[i][0] = left[i][1] = half[i][0] = half[i][1] = 1.0f;
-  Step st = {0, 32};
+  Step st = {0, 32, 0};
   for (int c = 0; c < nch;) {
     const int64_t tok = p.lo + (int64_t)(REV ? nch - 1 - c : c) * kScanC;
     const int nv = (int)min((int64_t)kScanC, p.hi - tok);
@@ -690,7 +707,7 @@ __global__ __launch_bounds__(NW * 64, NS > 4 ? 1 : 2) void scan_out_kernel(const
 #pragma unroll
     for (int w = 0; w < NW; ++w) all |= wild[w];
     if (st.width > 1 && __builtin_amdgcn_readfirstlane(all)) {
-      smaller(st);
+      smaller<REV>(st);
       __syncthreads();
       continue;
     }
@@ -703,10 +720,10 @@ __global__ __launch_bounds__(NW * 64, NS > 4 ? 1 : 2) void scan_out_kernel(const
     u32x4 vc[2];
     columns_of(vv, vc[0], vc[1]);
     const Step now = st;
-    advance(st);
+    advance<REV>(st);
     const int next = st.pos == kScanC ? c + 1 : c;
     if (next != c) {
-      st = Step{0, 32};
+      st = first_step<REV>(now);
       if (next < nch) fetch(next);   // in flight during the products
     }
     f32x4 o[2][2] = {};
@@ -920,7 +937,7 @@ __global__ __launch_bounds__(NW * 64, NV > 4 ? 1 : 2) void scan_grad_kernel(cons
   if (nch > 0) fetch(0);
   if (!REV) load_state();
   float left[2] = {1.0f, 1.0f};   // a step's second half e^{end-r}, done with the next step's first
-  Step st = {0, 32};
+  Step st = {0, 32, 0};
   for (int c = 0; c < nch;) {
     const int64_t tok = p.lo + (int64_t)(REV ? nch - 1 - c : c) * kScanC;
     const int nv = (int)min((int64_t)kScanC, p.hi - tok);
@@ -989,7 +1006,7 @@ __global__ __launch_bounds__(NW * 64, NV > 4 ? 1 : 2) void scan_grad_kernel(cons
 #pragma unroll
     for (int w = 0; w < NW; ++w) all |= wild[w];
     if (st.width > 1 && __builtin_amdgcn_readfirstlane(all)) {
-      smaller(st);
+      smaller<REV>(st);
       __syncthreads();
       continue;
     }
@@ -1002,10 +1019,10 @@ __global__ __launch_bounds__(NW * 64, NV > 4 ? 1 : 2) void scan_grad_kernel(cons
     uint32_t xw[8];
     load16<REV>(chunk_rsrc(a.X, xb, nv), xl, a.X.vec, xw);
     const Step now = st;
-    advance(st);
+    advance<REV>(st);
     const int next = st.pos == kScanC ? c + 1 : c;
     if (next != c) {
-      st = Step{0, 32};
+      st = first_step<REV>(now);
       if (next < nch) fetch(next);   // in flight during the products
     }
     f32x4 o[2][2] = {};

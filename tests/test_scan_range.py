@@ -65,3 +65,17 @@ def test_decays_of_a_segment_beyond_float32(scan, kind, gt, heads):  # noqa: F81
         x["g"][:, 300:308] = -12.0
         alone(x, 1e30, 1e30)
     check(x, *run(scan, x, heads))
+
+
+@pytest.mark.parametrize("kind", ["grow", "shrink"])
+@pytest.mark.parametrize("gt", [BF, F32], ids=["bf16", "f32gate"])
+def test_strong_token_behind_a_strong_half(scan, kind, gt):  # noqa: F811
+    """Half a chunk's decay of e^39 (e^-39) and a token's of e^60 (e^-85) right behind it, which is a
+    step of its own: their product is beyond float32, the state is not."""
+    x = tg.inputs(1, 90, 2, 64, 40, BF, gt)
+    x["g"][:] = 0
+    x["g"][:, 16:32] = 2.4375 if kind == "grow" else -2.4375
+    x["g"][:, 32] = 60.0 if kind == "grow" else -85.0
+    alone(x, *((1e-15, 1e-15) if kind == "grow" else (1e25, 1e25)))
+    o, ST = tg.fwd(scan, x)
+    check(x, o, ST, tg.bwd(scan, x))
