@@ -22,7 +22,7 @@
 // x e^{G-r} and k e^{r-G}: their product is the decay e^{G_i - G_j} of every
 // pair, and |G - r| <= kRange keeps each factor far from overflow.  Where that
 // does not hold (very strong gates, gates of -inf that clear the state) or a
-// value is not finite, the same code takes the chunk 8 tokens at a time, and
+// value is huge or not finite, the same code takes the chunk 8 tokens at a time, and
 // where it still does not, one token at a time, whose decay acts as a whole on
 // the state: no pair of factors is formed, so any gate will do and nothing
 // leaks from a later token into an earlier one.
@@ -59,7 +59,13 @@ typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
 constexpr int kScanC = 32;               // tokens per chunk
 constexpr float kRange = 40.0f;          // largest |G - r| of a chunk done as products
-constexpr float kBig = 1e37f;            // steps with larger factors are made smaller
+constexpr float kBig = 1e37f;            // larger factors are taken by the recurrence
+// Steps with larger factors (x e^{G-r}, k e^{r-G}) or values are made smaller: a
+// factor may be e^kRange times what its terms come to in the result, and the largest
+// sum before that is undone, of 32 tokens' factors times a score of two values over
+// 256 columns, is then at most 2^(66 + 5 + 23 + 23 + 8).  fp16 values are all smaller.
+constexpr float kFactor = 0x1p66f;
+constexpr uint32_t kValue = (127 + 23) << 7;   // 2^23 as the bits of a bf16 value
 
 // A (sequence, token, head, channel) tensor: element strides, channels dense.
 struct ScanTensor {
@@ -347,14 +353,14 @@ __device__ __forceinline__ void make_gates(const uint32_t (&w)[kGateWords<G32>],
 
 typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
 // The larger magnitudes of two pairs of 16-bit values, by their bits (NaN the
-// largest), and whether a pair holds one that is not finite.
+// largest), and whether a pair holds one that is too large for products or not finite.
 __device__ __forceinline__ uint32_t pair_max(uint32_t m, uint32_t w) {
   return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2, m),
                                                                 __builtin_bit_cast(u16x2, w & 0x7fff7fffu)));
 }
 template <int DT>
 __device__ __forceinline__ bool pair_wild(uint32_t m) {
-  constexpr uint32_t e = DT == DT_F16 ? 0x7c00u : 0x7f80u;
+  constexpr uint32_t e = DT == DT_F16 ? 0x7c00u : kValue;
   return (m & 0xffffu) >= e || (m >> 16) >= e;
 }
 
@@ -693,7 +699,7 @@ __global__ __launch_bounds__(NW * 64, NS > 4 ? 1 : 2) void scan_out_kernel(const
       }
       half[i][0] = q.b[0];
       half[i][1] = q.b[1];
-      hard |= q.hard || !(big <= kBig);   // NaN too
+      hard |= q.hard || !(big <= kFactor);   // NaN too
     }
     uint32_t vv[8], rawv = 0;
     take(st, g, vw, vv);
@@ -995,7 +1001,7 @@ __global__ __launch_bounds__(NW * 64, NV > 4 ? 1 : 2) void scan_grad_kernel(cons
         }
         big += __builtin_fabsf(kf[0][j]) + __builtin_fabsf(kf[1][j]);
       }
-      hard |= q.hard || !(big <= kBig);   // NaN too
+      hard |= q.hard || !(big <= kFactor);   // NaN too
       split8<3>(kf[0], kk[0]);
       split8<3>(kf[1], kk[1]);
     }

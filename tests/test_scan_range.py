@@ -79,3 +79,15 @@ def test_strong_token_behind_a_strong_half(scan, kind, gt):  # noqa: F811
     alone(x, *((1e-15, 1e-15) if kind == "grow" else (1e25, 1e25)))
     o, ST = tg.fwd(scan, x)
     check(x, o, ST, tg.bwd(scan, x))
+
+
+@pytest.mark.parametrize("which", ["v", "do", "k", "q"])
+@pytest.mark.parametrize("gt", [BF, F32], ids=["bf16", "f32gate"])
+def test_large_values_under_strong_gates(scan, which, gt):  # noqa: F811
+    """Values of 1e30 where half a chunk decays by e^-38: a factor of a product is e^38 times the
+    value, beyond float32, and every result is in range."""
+    x = tg.inputs(1, 70, 2, 64, 40, BF, gt, state=False)
+    x["g"][:] = -2.375
+    x[which] *= 1e30
+    o, ST = tg.fwd(scan, x)
+    check(x, o, ST, tg.bwd(scan, x))
