@@ -30,8 +30,8 @@
 // Precision: the products run on bf16 matrix instructions with fp32 sums, and
 // every fp32 factor enters as a sum of bf16 terms -- two (2^-17 relative) where
 // the result is rounded to 16 bits right after, three (2^-25) where it goes
-// into the fp32 state or a float32 gradient of the gates, which is a difference
-// of sums.  q, k, v and do are exact in one term (bf16) or two (f16).
+// into the fp32 state or the gradient of the gates, which is a running sum (two
+// there too if it and the tensors are bf16: see scan_grad_kernel).  q, k, v and do are exact in one term (bf16) or two (f16).
 //
 // Layout.  16x16x32 matrix instructions: an operand's lane (n = lane & 15,
 // g = lane >> 4) holds row/column n and the 8 depth positions 8g..8g+7; a
@@ -856,9 +856,13 @@ __global__ __launch_bounds__(NW * 64, NV > 4 ? 1 : 2) void scan_grad_kernel(cons
   constexpr int DVP = NV * 32, RS = DVP + kPadRow;
   constexpr int gb = G32 ? 4 : 2;
   constexpr int SL = (NV + NW - 1) / NW;        // slabs of 32 columns a wave stages
-  // terms of the state and the scores: two where everything is rounded to 16
-  // bits, three where the gates' gradient is kept in float32
-  constexpr int TP = G32 ? 3 : 2;
+  // terms of the state and the scores: three, as the gates' gradient is a running
+  // sum over the segment, and with two its errors show in an fp16 result (256 tokens
+  // and more) and in a float32 one at once.  bf16 tensors and gates take two: a
+  // term's error is below 2^-17 of it, so over t tokens sqrt(t) 2^-17, half a bf16
+  // step only after some 10^5 tokens of one segment (three: 338 for 330 us of
+  // gradients of 4 x 2048 tokens, 16 heads of 128 x 128).
+  constexpr int TP = G32 || DT == DT_F16 ? 3 : 2;
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
   uint16_t* vs = (uint16_t*)smem;               // V [32][RS]
   uint16_t* ws = vs + kScanC * RS;              // W [32][RS]

@@ -91,3 +91,23 @@ def test_large_values_under_strong_gates(scan, which, gt):  # noqa: F811
     x[which] *= 1e30
     o, ST = tg.fwd(scan, x)
     check(x, o, ST, tg.bwd(scan, x))
+
+
+@pytest.mark.parametrize("dt,gt", [(HF, HF), (HF, F32), (BF, F32)], ids=["f16", "f16_g32", "bf16_g32"])
+def test_gate_gradient_over_a_long_segment(scan, dt, gt):  # noqa: F811
+    """dg is a running sum: what the terms lose adds up over the sequence.  Here nothing is lost in 24
+    bits: no gates, no keys, S0 = (3 m, m) and output gradients (1, 0), (0, -1), (0, -1), (0, -1) in
+    turn, so every fourth dg, from the end, is exactly 0 and the others are multiples of m below 2^19."""
+    t, heads, dk = 4096, 1024, 32
+    x = tg.inputs(1, t, 1, dk, 2, dt, gt)
+    m = torch.randint(1 << 15, 1 << 16, (dk,), generator=torch.Generator().manual_seed(3)) * 2 + 1
+    x["S0"] = torch.stack([3 * m, m], 1).float()[None, None]
+    x["dST"], x["scale"] = None, 2.0 ** -20
+    x["k"][:], x["g"][:], x["q"][:], x["do"][:] = 0, 0, 1, 0
+    x["do"][:, 0::4, :, 0] = 1
+    for i in (1, 2, 3):
+        x["do"][:, i::4, :, 1] = -1
+    _, _, r = run(scan, x, heads)
+    left = torch.tensor([0, -3, -2, -1])[torch.arange(t) % 4]
+    want = (left[:, None] * m[None]).double() * 2.0 ** -20
+    assert torch.equal(r["dg"][0, :, 0].cpu(), want.to(gt))
