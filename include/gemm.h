@@ -22,7 +22,7 @@
  * y / (1 + e^-y).
  *
  * Layout: row-major with leading dimensions lda, ldb >= k, ldc, ldr >= n, in
- * elements; every tensor needs the alignment of its element only (16-byte
+ * elements (that of a single row is not used, nor limited below); every tensor needs the alignment of its element only (16-byte
  * aligned rows are faster).  C must not overlap anything else, except that
  * residual may be C itself with ldr == ldc.
  *

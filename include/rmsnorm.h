@@ -17,7 +17,8 @@
  * with a NaN gets a NaN scale; elements that are infinite, whose y is NaN, get
  * the code NaN, and the maximum is taken over the others.
  *
- * Layout: rows of leading dimension >= n, channels dense; 2-byte alignment
+ * Layout: rows of leading dimension >= n (that of a single row is not used),
+ * channels dense; 2-byte alignment
  * (scales 4-byte) is enough, 16-byte aligned rows are faster.  sum_out may be
  * x or residual, a 16-bit y may be x, each with the same leading dimension;
  * other overlaps with an output are refused.

@@ -113,6 +113,18 @@ GemmPlan gemm_plan(const gemm_t* p, bool whole) {
   return g;
 }
 
+// A lone row's leading dimension is never used (a row of a long sequence's last
+// token may have any): replaced by one that keeps 16-byte boundaries.
+gemm_t lone_rows(gemm_t p) {
+  const int64_t e = in_bytes(p.in_type), ld = up(p.k * e, 16) / e;
+  if (p.m == 1) {
+    p.lda = ld;
+    p.ldc = p.ldr = up(p.n, 8);
+  }
+  if (p.n == 1) p.ldb = ld;
+  return p;
+}
+
 bool whole_rows(const gemm_t* p, const void* A, const void* B) {
   const int64_t e = in_bytes(p->in_type);
   return ((((uintptr_t)A | (uintptr_t)B) & 15u) | ((p->lda * e) & 15) | ((p->ldb * e) & 15)) == 0;
@@ -122,8 +134,9 @@ Region matrix(const void* x, int64_t rows, int64_t cols, int64_t ld, int64_t byt
   return Region{(uintptr_t)x, bytes, {rows, 1, 1}, {ld, 0, 0}, cols};
 }
 
-gemv_status_t check(const gemm_t* p, const void* A, const void* B, const void* C, const void* workspace,
+gemv_status_t check(const gemm_t* given, const void* A, const void* B, const void* C, const void* workspace,
                     size_t workspace_bytes, bool sizes_only) {
+  const gemm_t* p = given;
   if (!p) return GEMV_ERR_INVALID_ARG;
   if (p->in_type < GEMM_F16 || p->in_type > GEMM_E4M3) return GEMV_ERR_UNSUPPORTED_DTYPE;
   if (p->dtype != GEMV_F16 && p->dtype != GEMV_BF16) return GEMV_ERR_UNSUPPORTED_DTYPE;
@@ -134,6 +147,8 @@ gemv_status_t check(const gemm_t* p, const void* A, const void* B, const void* C
   const int64_t e = in_bytes(p->in_type), lim = (int64_t)1 << 30;
   if (p->m > lim || p->n > lim || p->k > lim) return GEMV_ERR_TOO_LARGE;
   if (p->lda < p->k || p->ldb < p->k || p->ldc < p->n || (p->residual && p->ldr < p->n)) return GEMV_ERR_INVALID_ARG;
+  const gemm_t q = lone_rows(*given);
+  p = &q;
   if (p->lda > ((int64_t)1 << 23) / e || p->ldb > ((int64_t)1 << 23) / e || p->ldc > lim ||
       (p->residual && p->ldr > lim))
     return GEMV_ERR_TOO_LARGE;
@@ -186,12 +201,13 @@ extern "C" gemv_status_t gemm_check_args(const gemm_t* p, const void* A, const v
   return check(p, A, B, C, workspace, workspace_bytes, false);
 }
 
-extern "C" gemv_status_t gemm_run(gemv_handle_t h, const gemm_t* p, const void* A, const void* B, void* C,
+extern "C" gemv_status_t gemm_run(gemv_handle_t h, const gemm_t* given, const void* A, const void* B, void* C,
                                   void* workspace, size_t workspace_bytes, hipStream_t stream) {
   if (!h || h->magic != kMagic) return report(nullptr, GEMV_ERR_NULL_HANDLE, "gemm_run");
-  gemv_status_t st = check(p, A, B, C, workspace, workspace_bytes, false);
+  gemv_status_t st = check(given, A, B, C, workspace, workspace_bytes, false);
   if (st != GEMV_OK) return report(h, st, "gemm_run arguments");
-  if (p->m == 0 || p->n == 0) return GEMV_OK;
+  if (given->m == 0 || given->n == 0) return GEMV_OK;
+  const gemm_t q = lone_rows(*given), *p = &q;
   if ((st = mbd_host::ready(h, "gemm_run")) != GEMV_OK) return st;
   const GemmPlan g = gemm_plan(p, whole_rows(p, A, B));
   const int64_t e = in_bytes(p->in_type);

@@ -228,25 +228,35 @@ const Form kForms[] = {FORM(64, 1), FORM(64, 2), FORM(256, 1), FORM(256, 2), FOR
 const NormFn kAny[2][2] = {{&mbd::norm_any_kernel<0, false>, &mbd::norm_any_kernel<0, true>},
                            {&mbd::norm_any_kernel<1, false>, &mbd::norm_any_kernel<1, true>}};
 
+// A lone row's leading dimensions are never used: replaced by ones that keep
+// 16-byte boundaries.
+rmsnorm_t lone_row(rmsnorm_t p) {
+  if (p.m == 1) p.ldx = p.ldres = p.ldsum = p.ldy = (p.n + 7) / 8 * 8;
+  return p;
+}
+
 Region rows_of(const void* x, const rmsnorm_t* p, int64_t ld, int64_t bytes) {
   return Region{(uintptr_t)x, bytes, {p->m, 1, 1}, {ld, 0, 0}, p->n};
 }
 
 }  // namespace
 
-extern "C" gemv_status_t rmsnorm_check_args(const rmsnorm_t* p, const void* x, const void* residual, const void* w,
+extern "C" gemv_status_t rmsnorm_check_args(const rmsnorm_t* given, const void* x, const void* residual, const void* w,
                                             const void* sum_out, const void* y, const float* scales) {
+  const rmsnorm_t* p = given;
   if (!p) return GEMV_ERR_INVALID_ARG;
   if (p->dtype != GEMV_F16 && p->dtype != GEMV_BF16) return GEMV_ERR_UNSUPPORTED_DTYPE;
   if (p->out_e4m3 != 0 && p->out_e4m3 != 1) return GEMV_ERR_UNSUPPORTED_DTYPE;
   if (p->m < 0 || p->n < 0) return GEMV_ERR_INVALID_ARG;
   if (p->m == 0 || p->n == 0) return GEMV_OK;
   const int64_t lim = (int64_t)1 << 30;
-  if (p->m > ((int64_t)1 << 21) || p->n > ((int64_t)1 << 24) || p->ldx > lim || p->ldy > lim ||
-      (residual && p->ldres > lim) || (sum_out && p->ldsum > lim))
+  if (p->m > ((int64_t)1 << 21) || p->n > ((int64_t)1 << 24)) return GEMV_ERR_TOO_LARGE;
+  if (p->m > 1 && (p->ldx > lim || p->ldy > lim || (residual && p->ldres > lim) || (sum_out && p->ldsum > lim)))
     return GEMV_ERR_TOO_LARGE;
   if (p->ldx < p->n || p->ldy < p->n || (residual && p->ldres < p->n) || (sum_out && p->ldsum < p->n))
     return GEMV_ERR_INVALID_ARG;
+  const rmsnorm_t q = lone_row(*given);
+  p = &q;
   if (!x || !w || !y || (sum_out && !residual) || (p->out_e4m3 != 0) != (scales != nullptr))
     return GEMV_ERR_INVALID_ARG;
   if ((((uintptr_t)x | (uintptr_t)residual | (uintptr_t)w | (uintptr_t)sum_out) & 1u) ||
@@ -265,12 +275,13 @@ extern "C" gemv_status_t rmsnorm_check_args(const rmsnorm_t* p, const void* x, c
   return GEMV_OK;
 }
 
-extern "C" gemv_status_t rmsnorm_run(gemv_handle_t h, const rmsnorm_t* p, const void* x, const void* residual,
+extern "C" gemv_status_t rmsnorm_run(gemv_handle_t h, const rmsnorm_t* given, const void* x, const void* residual,
                                      const void* w, void* sum_out, void* y, float* scales, hipStream_t stream) {
   if (!h || h->magic != kMagic) return report(nullptr, GEMV_ERR_NULL_HANDLE, "rmsnorm_run");
-  gemv_status_t st = rmsnorm_check_args(p, x, residual, w, sum_out, y, scales);
+  gemv_status_t st = rmsnorm_check_args(given, x, residual, w, sum_out, y, scales);
   if (st != GEMV_OK) return report(h, st, "rmsnorm_run arguments");
-  if (p->m == 0 || p->n == 0) return GEMV_OK;
+  if (given->m == 0 || given->n == 0) return GEMV_OK;
+  const rmsnorm_t q = lone_row(*given), *p = &q;
   if ((st = mbd_host::ready(h, "rmsnorm_run")) != GEMV_OK) return st;
   mbd::NormArgs a = {(const uint16_t*)x, (const uint16_t*)residual, (const uint16_t*)w, (uint16_t*)sum_out, y, scales,
                      p->ldx, p->ldres, p->ldsum, p->ldy, (int32_t)p->n, p->eps};
