@@ -33,9 +33,10 @@
  * scratch: gemm_workspace_bytes says how much (possibly 0), any contents,
  * 16-byte aligned, not shared by calls that can overlap on the GPU.
  *
- * Limits (GEMV_ERR_TOO_LARGE): m, n, k <= 2^30; lda and ldb at most 2^23 bytes,
- * ldc and ldr at most 2^30 elements; gemm_run also where the tiles it picks are
- * more than a launch takes (beyond 2^36 outputs at the least).
+ * Limits (GEMV_ERR_TOO_LARGE): m, n, k <= 2^30, m n <= 2^38, and n <= 2^28 for
+ * up to 64 tokens; lda and ldb at most 2^23 bytes, ldc and ldr at most 2^30
+ * elements; also where the tiles that are picked are more than a launch takes
+ * (beyond 2^36 outputs at the least).
  */
 #ifndef MBD_GEMM_H
 #define MBD_GEMM_H

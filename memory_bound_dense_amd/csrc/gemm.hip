@@ -113,6 +113,11 @@ GemmPlan gemm_plan(const gemm_t* p, bool whole) {
   return g;
 }
 
+// Workgroups of the product and of the join.
+int64_t grid_of(const GemmPlan& g) { return g.tiles_m * g.tiles_n * g.nsplit; }
+int64_t join_grid_of(const gemm_t* p, const GemmPlan& g) { return g.nsplit > 1 ? (p->m * (g.npad / 4) + 255) / 256 : 0; }
+int threads_of(const GemmPlan& g) { return g.tile ? g.tile->threads : kSkinnyWaves * 64; }
+
 // A lone row's leading dimension is never used (a row of a long sequence's last
 // token may have any): replaced by one that keeps 16-byte boundaries.
 gemm_t lone_rows(gemm_t p) {
@@ -146,6 +151,8 @@ gemv_status_t check(const gemm_t* given, const void* A, const void* B, const voi
   if (p->m == 0 || p->n == 0) return GEMV_OK;
   const int64_t e = in_bytes(p->in_type), lim = (int64_t)1 << 30;
   if (p->m > lim || p->n > lim || p->k > lim) return GEMV_ERR_TOO_LARGE;
+  // more than 2^22 of the largest tiles (512 threads each) are no launch; what the plan works out stays below 2^63
+  if (p->m * p->n > (int64_t)1 << 38) return GEMV_ERR_TOO_LARGE;
   if (p->lda < p->k || p->ldb < p->k || p->ldc < p->n || (p->residual && p->ldr < p->n)) return GEMV_ERR_INVALID_ARG;
   const gemm_t q = lone_rows(*given);
   p = &q;
@@ -158,6 +165,9 @@ gemv_status_t check(const gemm_t* given, const void* A, const void* B, const voi
   if (e == 2 && p->k > 0) two |= (uintptr_t)A | (uintptr_t)B;
   if ((two & 1u) || (((uintptr_t)p->scale_a | (uintptr_t)p->scale_b) & 3u)) return GEMV_ERR_MISALIGNED;
   const GemmPlan g = gemm_plan(p, whole_rows(p, A, B));
+  // a grid's work-items along x (a 32-bit field of the dispatch) are kept at most 2^31
+  if (grid_of(g) > ((int64_t)1 << 31) / threads_of(g) || join_grid_of(p, g) > ((int64_t)1 << 23))
+    return GEMV_ERR_TOO_LARGE;
   if (g.bytes) {
     if (!workspace || workspace_bytes < g.bytes) return GEMV_ERR_INVALID_ARG;
     if ((uintptr_t)workspace & 15u) return GEMV_ERR_MISALIGNED;
@@ -237,17 +247,11 @@ extern "C" gemv_status_t gemm_run(gemv_handle_t h, const gemm_t* given, const vo
   a.npad = (int32_t)g.npad;
   a.once = (((uintptr_t)B | (uint64_t)a.ldb) & 127u) == 0;
   a.alpha = p->alpha;
-  const int64_t grid = g.tiles_m * g.tiles_n * g.nsplit;
-  const int threads = g.tile ? g.tile->threads : kSkinnyWaves * 64;
-  const int64_t jgrid = g.nsplit > 1 ? (p->m * (g.npad / 4) + 255) / 256 : 0;
-  // a grid's work-items along x (a 32-bit field of the dispatch) are kept at most 2^31
-  if (grid > ((int64_t)1 << 31) / threads || jgrid > ((int64_t)1 << 23))
-    return report(h, GEMV_ERR_TOO_LARGE, "gemm_run grid");
   void* args[] = {(void*)&a};
   const void* fn = (const void*)(g.tile ? g.tile->fn[p->in_type] : kSkinny[g.rt][g.mt][p->in_type]);
-  hipError_t err = hipLaunchKernel(fn, dim3((unsigned)grid), dim3((unsigned)threads), args,
+  hipError_t err = hipLaunchKernel(fn, dim3((unsigned)grid_of(g)), dim3((unsigned)threads_of(g)), args,
                                    g.tile ? g.tile->lds : 0, stream);
   if (err == hipSuccess && g.nsplit > 1)
-    err = hipLaunchKernel((const void*)&mbd::gemm_join_kernel, dim3((unsigned)jgrid), dim3(256), args, 0, stream);
+    err = hipLaunchKernel((const void*)&mbd::gemm_join_kernel, dim3((unsigned)join_grid_of(p, g)), dim3(256), args, 0, stream);
   return err == hipSuccess ? GEMV_OK : report(h, GEMV_ERR_HIP, hipGetErrorString(err));
 }
