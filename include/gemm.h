@@ -69,6 +69,16 @@ size_t gemm_workspace_bytes(const gemm_t* p);
 gemv_status_t gemm_run(gemv_handle_t h, const gemm_t* p, const void* A, const void* B, void* C,
                        void* workspace, size_t workspace_bytes, hipStream_t stream);
 
+/* What gemm_run picks for a call, worked out on the host alone (no handle, no GPU);
+ * of A and B only the alignment is looked at.  GEMV_ERR_INVALID_ARG without p or
+ * out, gemm_run's statuses for sizes that it refuses, zeros where it does nothing. */
+typedef struct {
+  int32_t rows, tokens;    /* outputs per workgroup: rows of B x tokens */
+  int32_t kind;            /* 0 few tokens, 1 tiles through registers, 2 tiles by loads into LDS */
+  int32_t splits;          /* of k over workgroups */
+} gemm_config_t;
+gemv_status_t gemm_plan_config(const gemm_t* p, const void* A, const void* B, gemm_config_t* out);
+
 /* The host checks of gemm_run, in its order (no handle, no GPU). */
 gemv_status_t gemm_check_args(const gemm_t* p, const void* A, const void* B, const void* C,
                               const void* workspace, size_t workspace_bytes);

@@ -10,7 +10,7 @@ from ._lib import (EXPORTS, GEMV_BF16, GEMV_F16, GEMV_OK, Gemv, GemvError, GlaDe
                    gemv_num_variants, gemv_plan_config, gemv_query_config, gemv_run,
                    gemv_run_ex, gemv_run_noalloc, gemv_run_ws, gemv_status_string, gemv_variant_info, load)
 from ._operators import (GEMM_ACTS, GEMM_BF16, GEMM_E4M3, GEMM_F16, OPERATOR_EXPORTS, Gemm, GlaScan,
-                         RmsNorm, gemm_check_args, gemm_run, gemm_t, gemm_workspace_bytes,
+                         RmsNorm, gemm_check_args, gemm_config_t, gemm_plan_config, gemm_run, gemm_t, gemm_workspace_bytes,
                          gla_scan_backward, gla_scan_check_args, gla_scan_forward,
                          gla_scan_grad_check_args, gla_scan_grad_t, gla_scan_t,
                          gla_scan_workspace_bytes, gla_stride_t, operators_prepare, rmsnorm_check_args, rmsnorm_run,
@@ -23,7 +23,7 @@ __all__ = ["EXPORTS", "GEMV_BF16", "GEMV_F16", "GEMV_OK", "Gemv", "GemvError", "
            "gemv_run_noalloc", "gemv_run_ws",
            "gemv_status_string", "gemv_variant_info", "load",
            "GEMM_ACTS", "GEMM_BF16", "GEMM_E4M3", "GEMM_F16", "Gemm", "RmsNorm",
-           "gemm_check_args", "gemm_run", "gemm_t", "gemm_workspace_bytes", "rmsnorm_check_args",
+           "gemm_check_args", "gemm_config_t", "gemm_plan_config", "gemm_run", "gemm_t", "gemm_workspace_bytes", "rmsnorm_check_args",
            "rmsnorm_run", "rmsnorm_t", "OPERATOR_EXPORTS", "GlaScan", "gla_scan_backward", "gla_scan_check_args",
            "gla_scan_forward", "gla_scan_grad_check_args", "gla_scan_grad_t", "gla_scan_t",
            "gla_scan_workspace_bytes", "gla_stride_t", "operators_prepare"]

@@ -23,7 +23,7 @@ LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libmbd_oper
 # every symbol these headers declare
 OPERATOR_EXPORTS = ("operators_prepare", "gla_scan_workspace_bytes", "gla_scan_forward", "gla_scan_backward",
                     "gla_scan_check_args", "gla_scan_grad_check_args", "gemm_workspace_bytes",
-                    "gemm_run", "gemm_check_args", "rmsnorm_run", "rmsnorm_check_args")
+                    "gemm_run", "gemm_plan_config", "gemm_check_args", "rmsnorm_run", "rmsnorm_check_args")
 
 GEMM_F16, GEMM_BF16, GEMM_E4M3 = 0, 1, 2
 GEMM_ACTS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
@@ -54,6 +54,10 @@ class gemm_t(ctypes.Structure):
                 ("scale_a", _vp), ("scale_b", _vp), ("bias", _vp), ("residual", _vp)]
 
 
+class gemm_config_t(ctypes.Structure):
+    _fields_ = [("rows", _i32), ("tokens", _i32), ("kind", _i32), ("splits", _i32)]
+
+
 class rmsnorm_t(ctypes.Structure):
     _fields_ = [("m", _i64), ("n", _i64), ("ldx", _i64), ("ldres", _i64), ("ldsum", _i64),
                 ("ldy", _i64), ("dtype", _st), ("out_e4m3", _i32), ("eps", _f32)]
@@ -82,6 +86,7 @@ def load():
         lib.gemm_workspace_bytes.argtypes = [gemm]
         lib.gemm_workspace_bytes.restype = _sz
         lib.gemm_run.argtypes = [_vp, gemm, _vp, _vp, _vp, _vp, _sz, _vp]
+        lib.gemm_plan_config.argtypes = [gemm, _vp, _vp, ctypes.POINTER(gemm_config_t)]
         lib.gemm_check_args.argtypes = [gemm, _vp, _vp, _vp, _vp, _sz]
         lib.rmsnorm_run.argtypes = [_vp, norm] + [_vp] * 7
         lib.rmsnorm_check_args.argtypes = [norm] + [_vp] * 6
@@ -132,6 +137,13 @@ def gemm_workspace_bytes(p):
 
 def gemm_run(h, p, A, B, C, workspace=None, workspace_bytes=0, stream=None):
     return load().gemm_run(h, ctypes.byref(p), A, B, C, workspace, workspace_bytes, stream)
+
+
+def gemm_plan_config(p, A=None, B=None):
+    """What gemm_run picks for a call, on the host alone (no device); A and B: addresses."""
+    cfg = gemm_config_t()
+    s = load().gemm_plan_config(ctypes.byref(p), A, B, ctypes.byref(cfg))
+    return s, cfg
 
 
 def gemm_check_args(p, A, B, C, workspace=None, workspace_bytes=0):

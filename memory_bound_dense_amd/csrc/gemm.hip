@@ -24,16 +24,17 @@ using GemmFn = void (*)(const mbd::GemmArgs);
 // for 16 a CU.
 struct Tile {
   int bn, bm, threads;
+  bool direct;       // loads straight into LDS
   size_t lds;        // dynamic
   int alone, shared;
   GemmFn fn[3];
 };
 #define TILE(BN, BM, WN, WM, ALONE, SHARED)                                                         \
-  {BN, BM, WN * WM * 64, mbd::gemm_tile_lds<BN, BM>(), ALONE, SHARED,                               \
+  {BN, BM, WN * WM * 64, false, mbd::gemm_tile_lds<BN, BM>(), ALONE, SHARED,                               \
    {&mbd::gemm_tile_kernel<0, BN, BM, WN, WM>, &mbd::gemm_tile_kernel<1, BN, BM, WN, WM>,           \
     &mbd::gemm_tile_kernel<2, BN, BM, WN, WM>}}
 #define DIRECT(BN, BM, WN, WM, WK, WN8, WM8, ST, ALONE, SHARED)                                                 \
-  {BN, BM, WN * WM * WK * 64, 0, ALONE, SHARED,                                                                 \
+  {BN, BM, WN * WM * WK * 64, true, 0, ALONE, SHARED,                                                                 \
    {&mbd::gemm_direct_kernel<0, BN, BM, WN, WM, WK, ST>, &mbd::gemm_direct_kernel<1, BN, BM, WN, WM, WK, ST>,   \
     &mbd::gemm_direct_kernel<2, BN, BM, WN8, WM8, 1, ST>}}
 // [1]: rows on 16-byte boundaries
@@ -117,6 +118,10 @@ GemmPlan gemm_plan(const gemm_t* p, bool whole) {
 int64_t grid_of(const GemmPlan& g) { return g.tiles_m * g.tiles_n * g.nsplit; }
 int64_t join_grid_of(const gemm_t* p, const GemmPlan& g) { return g.nsplit > 1 ? (p->m * (g.npad / 4) + 255) / 256 : 0; }
 int threads_of(const GemmPlan& g) { return g.tile ? g.tile->threads : kSkinnyWaves * 64; }
+// A grid's work-items along x (a 32-bit field of the dispatch) are kept at most 2^31.
+bool launchable(const gemm_t* p, const GemmPlan& g) {
+  return grid_of(g) <= ((int64_t)1 << 31) / threads_of(g) && join_grid_of(p, g) <= ((int64_t)1 << 23);
+}
 
 // A lone row's leading dimension is never used (a row of a long sequence's last
 // token may have any): replaced by one that keeps 16-byte boundaries.
@@ -165,9 +170,7 @@ gemv_status_t check(const gemm_t* given, const void* A, const void* B, const voi
   if (e == 2 && p->k > 0) two |= (uintptr_t)A | (uintptr_t)B;
   if ((two & 1u) || (((uintptr_t)p->scale_a | (uintptr_t)p->scale_b) & 3u)) return GEMV_ERR_MISALIGNED;
   const GemmPlan g = gemm_plan(p, whole_rows(p, A, B));
-  // a grid's work-items along x (a 32-bit field of the dispatch) are kept at most 2^31
-  if (grid_of(g) > ((int64_t)1 << 31) / threads_of(g) || join_grid_of(p, g) > ((int64_t)1 << 23))
-    return GEMV_ERR_TOO_LARGE;
+  if (!launchable(p, g)) return GEMV_ERR_TOO_LARGE;
   if (g.bytes) {
     if (!workspace || workspace_bytes < g.bytes) return GEMV_ERR_INVALID_ARG;
     if ((uintptr_t)workspace & 15u) return GEMV_ERR_MISALIGNED;
@@ -204,6 +207,19 @@ extern "C" size_t gemm_workspace_bytes(const gemm_t* p) {
   if (check(p, nullptr, nullptr, nullptr, nullptr, 0, true) != GEMV_OK || p->m == 0 || p->n == 0) return 0;
   // the pointers are not known here: what either kind of rows needs
   return std::max(gemm_plan(p, false).bytes, gemm_plan(p, true).bytes);
+}
+
+extern "C" gemv_status_t gemm_plan_config(const gemm_t* p, const void* A, const void* B, gemm_config_t* out) {
+  if (!out) return GEMV_ERR_INVALID_ARG;
+  *out = gemm_config_t{};
+  const gemv_status_t st = check(p, nullptr, nullptr, nullptr, nullptr, 0, true);
+  if (st != GEMV_OK || p->m == 0 || p->n == 0) return st;
+  const gemm_t q = lone_rows(*p);
+  const GemmPlan g = gemm_plan(&q, whole_rows(&q, A, B));
+  if (!launchable(&q, g)) return GEMV_ERR_TOO_LARGE;
+  if (g.tile) *out = gemm_config_t{g.tile->bn, g.tile->bm, g.tile->direct ? 2 : 1, (int32_t)g.nsplit};
+  else *out = gemm_config_t{16 * (g.rt + 1), 16 << g.mt, 0, (int32_t)g.nsplit};
+  return GEMV_OK;
 }
 
 extern "C" gemv_status_t gemm_check_args(const gemm_t* p, const void* A, const void* B, const void* C,
