@@ -311,10 +311,11 @@ struct Gates {
   bool hard;
 };
 // Decays are products of the gates' exponentials, from the middle of the chunk
-// outwards: each factor is within about 2^-24, so a decay over i tokens within
-// about sqrt(i) 2^-24, whatever its size (a sum of gates in fp32, |G| = 20,
-// loses 1e-6), and an element costs one exponential, one reciprocal and three
-// products.
+// outwards: an element costs one exponential, one reciprocal and three products.
+// A token's factor is within (1.3 |g| + 3) 2^-24: its argument g log2(e) is rounded
+// once (and the constant is off by 0.23 2^-24), the exponential is within one unit,
+// its product rounds once.  Over the tokens of a decay these add up, for equal
+// gates linearly, as in the recurrence itself; a gate of 0 is exact.
 template <int DT, bool G32, bool REV>
 __device__ __forceinline__ void make_gates(const uint32_t (&w)[kGateWords<G32>], int lane, Gates& q) {
   const int g = lane >> 4;
