@@ -138,3 +138,21 @@ def test_every_form_of_few_tokens(h, rows, tokens, m, n, t, dt):
         check(h, t, dt, m, n, k, (k + 127) // 128 * 128)
     k = depth(t, 300, True)
     check(h, t, dt, m, 100, k, strides(t, False, k))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("m,n,k", [(16, 300, 4096), (64, 100, 9000), (300, 1000, 2048), (2048, 4096, 328)])
+def test_bits_go_by_sizes_and_alignment_alone(h, m, n, k):
+    """Rows on 16-byte boundaries at any leading dimension, and rows off them at any: the same bits
+    each; up to 64 tokens all the same."""
+    mm = mbd.Gemm(h)
+    A, B = (torch.randn(r, k, generator=torch.Generator().manual_seed(r)).to(BF).cuda() for r in (m, n))
+    got = []
+    for ld in (k, k + 8, k + 200, k + 1, k + 6):
+        C = torch.empty(m, n, dtype=BF, device="cuda")
+        mm(rows_in(A, ld), rows_in(B, ld), C)
+        got.append(C)
+    torch.cuda.synchronize()
+    assert torch.equal(got[0], got[1]) and torch.equal(got[0], got[2]) and torch.equal(got[3], got[4])
+    if m <= 64:
+        assert torch.equal(got[0], got[3])
