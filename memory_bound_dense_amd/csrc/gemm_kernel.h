@@ -287,7 +287,7 @@ __device__ __forceinline__ void write_tile(const GemmArgs& p, const f32x4 (&c)[T
 // Bound by HBM: 16 tokens, n = 11008, k = 4096 in bf16 with cold weights 17.2 us
 // (5.2 TB/s, what a large copy reaches).  A ring of 4 slabs and 16 waves were
 // slower.  Rows that do not begin on a line share each line between two slabs:
-// then lines are kept for the next one (16 tokens, n = 4097, k = 4099: 13.4 us
+// then lines are kept for the next one (16 tokens, n = 4097, k = 4099: 13.7 us
 // for 19.1; n = 18432, k = 7169: 85 for 91), which costs where they are not
 // shared (n = 18432, k = 7168: 55 for 52).
 

@@ -1,5 +1,6 @@
-// Internal to libgemv.so: the handle shared by the GEMV (gemv.hip) and the
-// GLA decode step (gla.hip), and error reporting.
+// Internal: the handle that libgemv.so makes and its GEMV (gemv.hip), its GLA
+// decode step (gla.hip) and the operators of libmbd_operators.so share, and
+// error reporting.  Both libraries are built from this layout.
 #pragma once
 
 #include <stdint.h>
