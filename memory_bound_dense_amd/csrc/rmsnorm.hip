@@ -90,7 +90,7 @@ struct RowScale {
 __device__ __forceinline__ RowScale row_scale(const NormArgs& p, float ss, float mx) {
   RowScale s;
   s.r = 1.0f / sqrtf(ss / (float)p.n + p.eps);
-  s.scale = s.r * mx / 448.0f;
+  s.scale = ss == 0.0f && mx == 0.0f ? 0.0f : s.r * mx / 448.0f;   // r is infinite if eps is 0 too
   s.up = mx < 0x1p-100f ? 0x1p100f : 1.0f;
   s.inv = mx > 0.0f ? 448.0f / (mx * s.up) : 0.0f;
   return s;
