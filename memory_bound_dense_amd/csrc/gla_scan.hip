@@ -164,7 +164,7 @@ bool strides_fit(const gla_scan_t* p, const gla_stride_t& s, int64_t d) {
   const int64_t t = p->offsets ? p->rows : p->tokens;
   if (s.head < 0 || s.head > ((int64_t)1 << 40)) return false;
   if (!p->offsets && (s.batch < 0 || s.batch > ((int64_t)1 << 40))) return false;
-  return t <= 1 ? (s.token >= 0 && s.token <= kMaxStride) : (s.token >= d && s.token <= kMaxStride);
+  return t <= 1 || (s.token >= d && s.token <= kMaxStride);   // one token's stride is not used
 }
 
 // Sizes and scalars; *idle: nothing to do.

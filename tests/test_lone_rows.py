@@ -1,11 +1,14 @@
-"""A product or norm of one row takes that row from anywhere: its leading
-dimension is never used, so it is neither limited nor chooses a kernel."""
+"""A product or norm of one row, and a scan of one token, take it from anywhere:
+its leading dimension or token stride is never used, so it is neither limited nor
+chooses a kernel."""
 import pytest
 import torch
 
 import memory_bound_dense_amd as mbd
 import test_gemm
-from test_operator_args import INVALID, OK, TOO_LARGE, at, gcheck, gemm, ncheck, norm
+import test_gla_scan as tg
+from memory_bound_dense_amd import _operators as ops
+from test_operator_args import INVALID, OK, TOO_LARGE, at, bwd, fwd, gcheck, gemm, grads, ncheck, norm, scan
 
 BF, HF, E4 = torch.bfloat16, torch.float16, torch.float8_e4m3fn
 
@@ -26,6 +29,20 @@ def test_leading_dimensions_of_single_rows_are_not_limited():
     assert ncheck(norm(m=1, ldx=far, ldres=far, ldsum=far, ldy=far), res=r, s=s) == OK
     assert ncheck(norm(m=1, ldsum=far), res=r, s=at(0)) == OK                   # in place
     assert ncheck(norm(m=2, ldx=far)) == TOO_LARGE and ncheck(norm(m=1, ldx=31)) == INVALID
+
+
+def test_the_token_stride_of_one_token_is_not_limited():
+    for packed in (False, True):
+        for st in (0, 1 << 25, 1 << 40):
+            p = scan(b=1 if packed else 2, t=1)
+            for n in ("q", "k", "v", "gk", "o"):
+                s = getattr(p, n)
+                setattr(p, n, ops.gla_stride_t(s.batch, st, s.head))
+            if packed:
+                p.offsets, p.rows = at(15), 1
+            assert fwd(p) == OK and bwd(p, grads(p)) == OK
+            p.tokens = p.rows = 2
+            assert fwd(p) == INVALID
 
 
 @pytest.fixture(scope="module")
@@ -84,3 +101,23 @@ def test_single_rows_of_any_stride(h, stride, shift):
         got.append(torch.cat([y, s]))
     torch.cuda.synchronize()
     assert torch.equal(*got)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("stride", [1 << 25, 1 << 33])
+def test_one_token_of_a_far_stride(h, stride):
+    """The first token of (tokens, batch, ...) tensors whose tokens are far apart."""
+    x = tg.cuda(tg.inputs(2, 1, 3, 64, 40, BF, BF, seed=2))
+    sc = mbd.GlaScan(h)
+    got = []
+    for far in (False, True):
+        like = lambda t: torch.as_strided(t, t.shape, (t.stride(0), stride, t.stride(2), 1)) if far else t
+        o, ST, dS0 = torch.empty_like(x["v"]), torch.empty_like(x["S0"]), torch.empty_like(x["S0"])
+        r = [torch.empty_like(x[n]) for n in ("q", "k", "v", "g")]
+        y = [like(x[n]) for n in ("q", "k", "v", "g", "do")]
+        sc.forward(*y[:4], like(o), x["scale"], S0=x["S0"], ST=ST)
+        sc.backward(*y, *[like(t) for t in r], x["scale"], S0=x["S0"], dST=x["dST"], dS0=dS0)
+        got.append([o, ST, dS0] + r)
+    torch.cuda.synchronize()
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
