@@ -54,7 +54,8 @@
  * depend on timing.
  *
  * Limits (GEMV_ERR_TOO_LARGE): dk <= 256; dv <= 65536 forward, 256 backward;
- * tokens, rows <= 2^30; batch * heads <= 2^20.  batch, heads, dk or dv of 0 is
+ * tokens, rows <= 2^30; batch * heads <= 2^20, and times ceil(dv / 128) <= 2^23
+ * forward; batch * tokens <= 2^34 unless packed.  batch, heads, dk or dv of 0 is
  * a no-op, as is tokens == 0 without ST / dS0.
  */
 #ifndef MBD_GLA_SCAN_H

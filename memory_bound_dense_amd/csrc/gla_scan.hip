@@ -208,6 +208,18 @@ gemv_status_t check_scratch(const ScanPlan& s, const void* workspace, size_t byt
   return GEMV_OK;
 }
 
+// A grid's work-items along x (a 32-bit field of the dispatch) are kept at most 2^31.
+bool grid_fits(int64_t grid, int threads) { return grid <= ((int64_t)1 << 31) / threads; }
+
+// Workgroups of the outputs, and of the gradients over the key channels.
+int64_t out_grid(const gla_scan_t* p, const ScanPlan& s) {
+  return s.heads * s.nseg * ((p->dv + out_cols(p->dv) - 1) / out_cols(p->dv));
+}
+int64_t grad_grid(const gla_scan_t* p, const ScanPlan& s) {
+  const int64_t cols = 32 * waves_of(p->dk);
+  return s.heads * s.nseg * ((p->dk + cols - 1) / cols);
+}
+
 // Outputs against each other and against the inputs.
 bool clash(const Region* out, int no, const Region* in, int ni) {
   for (int i = 0; i < no; ++i) {
@@ -230,6 +242,7 @@ gemv_status_t check_forward(const gla_scan_t* p, const void* q, const void* k, c
   if (st != GEMV_OK) return st;
   if (((uintptr_t)S0 | (uintptr_t)ST) & 3u) return GEMV_ERR_MISALIGNED;
   const ScanPlan s = scan_plan(p, false);
+  if (!grid_fits(out_grid(p, s), 256)) return GEMV_ERR_TOO_LARGE;
   st = check_scratch(s, workspace, workspace_bytes);
   if (st != GEMV_OK) return st;
   const int64_t state = s.heads * p->dk * p->dv, gb = p->gate_f32 ? 4 : 2;
@@ -261,6 +274,7 @@ gemv_status_t check_backward(const gla_scan_t* p, const gla_scan_grad_t* gr, con
   if (((uintptr_t)dgk & (p->gate_f32 ? 3u : 1u)) || (((uintptr_t)S0 | (uintptr_t)dST | (uintptr_t)dS0) & 3u))
     return GEMV_ERR_MISALIGNED;
   const ScanPlan s = scan_plan(p, true);
+  if (!grid_fits(out_grid(p, s), 256) || !grid_fits(grad_grid(p, s), 256)) return GEMV_ERR_TOO_LARGE;
   st = check_scratch(s, workspace, workspace_bytes);
   if (st != GEMV_OK) return st;
   const int64_t state = s.heads * p->dk * p->dv, gb = p->gate_f32 ? 4 : 2;
@@ -352,9 +366,6 @@ hipError_t launch_join(const ScanPlan& s, const mbd::JoinArgs& j, int sides, hip
                          dim3(256), args, 0, stream);
 }
 
-// A grid's work-items along x (a 32-bit field of the dispatch) are kept at most 2^31.
-bool grid_fits(int64_t grid, int threads) { return grid <= ((int64_t)1 << 31) / threads; }
-
 }  // namespace
 
 bool mbd_host::scan_set_attributes() {
@@ -419,8 +430,6 @@ extern "C" gemv_status_t gla_scan_forward(gemv_handle_t h, const gla_scan_t* p, 
   a.ST = ST;
   a.cols = out_cols(p->dv);
   a.nblk = (int32_t)((p->dv + a.cols - 1) / a.cols);
-  const int64_t grid = bh * s.nseg * a.nblk;
-  if (!grid_fits(grid, 256)) return report(h, GEMV_ERR_TOO_LARGE, "gla_scan_forward grid");
   hipError_t e = hipSuccess;
   if (s.nseg > 1) {
     char* w = (char*)workspace;
@@ -441,7 +450,7 @@ extern "C" gemv_status_t gla_scan_forward(gemv_handle_t h, const gla_scan_t* p, 
     if (e == hipSuccess) e = launch_join(s, {{join_of(p, s, a.slots, a.decays, S0, 0), {}}}, 1, stream);
   }
   const int ow = waves_of(a.cols);
-  if (e == hipSuccess) e = launch(scan_form(kScanOut, p, 0, tier(p->dk), ow == 4), grid, ow, kOutLds[tier(p->dk)], a, stream);
+  if (e == hipSuccess) e = launch(scan_form(kScanOut, p, 0, tier(p->dk), ow == 4), out_grid(p, s), ow, kOutLds[tier(p->dk)], a, stream);
   return e == hipSuccess ? GEMV_OK : report(h, GEMV_ERR_HIP, hipGetErrorString(e));
 }
 
@@ -494,9 +503,7 @@ extern "C" gemv_status_t gla_scan_backward(gemv_handle_t h, const gla_scan_t* p,
   o.ST = nullptr;
   o.cols = cols;
   o.nblk = (int32_t)((p->dv + cols - 1) / cols);
-  const int64_t gk_grid = s.heads * s.nseg * f.nblk, gv_grid = s.heads * s.nseg * o.nblk;
-  if (!grid_fits(gk_grid, 256) || !grid_fits(gv_grid, 256))
-    return report(h, GEMV_ERR_TOO_LARGE, "gla_scan_backward grid");
+  const int64_t gk_grid = grad_grid(p, s), gv_grid = out_grid(p, s);
   hipError_t e = hipSuccess;
   if (s.nseg > 1) {
     f.slots = (float*)(w + s.slots);
