@@ -1156,6 +1156,13 @@ __global__ __launch_bounds__(NW * 64, NV > 4 ? 1 : 2) void scan_grad_kernel(cons
         carry[nt] += __shfl(s, 48 + n, 64);
 #pragma unroll
         for (int j = 0; j < 8; ++j) d[nt][j] += base;
+        // A gate whose factor is 0 has no gradient; the sum's error of the tokens behind it
+        // stays there too.  (A NaN goes on.)
+        if (now.width == 1 && left[nt] == 0.0f) {
+          carry[nt] *= 0.0f;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) d[nt][j] *= 0.0f;
+        }
       }
 #pragma unroll
       for (int j = 0; j < 8; ++j) {

@@ -111,3 +111,20 @@ def test_gate_gradient_over_a_long_segment(scan, dt, gt):  # noqa: F811
     left = torch.tensor([0, -3, -2, -1])[torch.arange(t) % 4]
     want = (left[:, None] * m[None]).double() * 2.0 ** -20
     assert torch.equal(r["dg"][0, :, 0].cpu(), want.to(gt))
+
+
+@pytest.mark.parametrize("heads", [4, 1024])
+@pytest.mark.parametrize("dt,gt", tg.TYPES, ids=tg.TIDS)
+def test_gate_gradient_before_a_reset(scan, dt, gt, heads):  # noqa: F811
+    """Two texts with a gate of -inf between them, the second's values 64 times the first's: the first
+    one's results, the gates' gradient too, are held to the bounds that it has alone."""
+    x = tg.inputs(1, 300, 1, 32, 32, dt, gt, gate=4.0)
+    x["g"][:, 150] = -float("inf")
+    for n in ("q", "k", "v", "do"):
+        x[n][:, 150:] *= 64
+    o, ST, r = run(scan, x, heads)
+    first = {n: y[:, :150] if torch.is_tensor(y) and y.shape[1] == 300 else y for n, y in x.items()}
+    first["dST"] = None
+    rows = {n: y[:, :150] if n != "dS0" else y for n, y in r.items()}
+    assert (r["dg"][:, 150] == 0).all()
+    check(first, o[:, :150], None, rows)
