@@ -9,7 +9,8 @@
 //     last token is dS_T),  dv_t = D_t^T k_t,  dk_t = D_t v_t,
 //     dq_t = scale S_t do_t,  dg_t = dg_{t+1} + q_t dq_t - k_t dk_t
 //
-// (the last because rowsum(S_t D_t) = dg_t + k_t dk_t = dg_{t+1} + q_t dq_t).
+// (the last because rowsum(S_t D_t) = dg_t + k_t dk_t = dg_{t+1} + q_t dq_t; the
+// token's own term, the same in both, is left out of them).
 // Reversed, a recurrence differs from the forward one only in its order and
 // in that a token's gate acts after the token instead of before it, so the same
 // kernels serve both:
@@ -543,6 +544,20 @@ __device__ __forceinline__ void get_scores(const uint8_t* ps, int it, int lane, 
   for (int m = 0; m < TERMS; ++m) x[m] = *(const bf16x8*)(ps + ((it * TERMS + m) * 64 + lane) * 16);
 }
 
+// Scores without those of a token with itself.
+template <int TERMS>
+__device__ __forceinline__ void drop_own(bf16x8 (&x)[TERMS], int it, int lane) {
+  const int n = lane & 15, g = lane >> 4;   // token row_of(n, it) is position 4 it + n % 4 of group n / 4
+  const uint32_t keep = g != n >> 2 ? 0xffffffffu : n & 1 ? 0x0000ffffu : 0xffff0000u;
+#pragma unroll
+  for (int m = 0; m < TERMS; ++m) {
+    u32x4 w = __builtin_bit_cast(u32x4, x[m]);
+    w[2 * it] &= n & 2 ? 0xffffffffu : keep;
+    w[2 * it + 1] &= n & 2 ? keep : 0xffffffffu;
+    x[m] = __builtin_bit_cast(bf16x8, w);
+  }
+}
+
 // ---- out_i = X_i^T S ---------------------------------------------------------
 // With S the state before the chunk, in units of e^{-r}:
 //     out = X' S + tril(X' K'^T) V,  S <- S + K'^T V,  X' = X e^{G-r}, K' = K e^{r-G}
@@ -838,7 +853,11 @@ __global__ __launch_bounds__(NW * 64, NS > 4 ? 1 : 2) void scan_out_kernel(const
 }
 
 // ---- out_i = S W_i ------------------------------------------------------------
-// out_i = e^{G_i - r} (S W_i + sum_j tril(W_i . V_j) K'_j), and with it dg.
+// out_i = e^{G_i - r} (S W_i + sum_j tril(W_i . V_j) K'_j), and with it dg.  A token's
+// own term (j = i) is the same in q dq and in k dk: it is left out of both and added
+// to the output alone.  Under strong gates it is nearly all of them, and the
+// rounding that it left behind when it cancelled outweighed dg (gates of -10 to
+// -7, 4096 tokens: 0.44 of dg in bf16, 0.010 in float32).
 // A wave owns 32 channels (columns of the transposed state, 64 VGPRs at DV
 // 128) and their part of the output; K e^{r-G} of its channels never leaves
 // its registers.  V and W go through LDS, row-major for the products over DV
@@ -861,7 +880,8 @@ __global__ __launch_bounds__(NW * 64, NV > 4 ? 1 : 2) void scan_grad_kernel(cons
   // sum over the segment, and with two its errors show in an fp16 result (256 tokens
   // and more) and in a float32 one at once.  bf16 tensors and gates take two: a
   // term's error is below 2^-17 of it, so over t tokens sqrt(t) 2^-17, half a bf16
-  // step only after some 10^5 tokens of one segment (three: 338 for 330 us of
+  // step only after some 10^5 tokens of one segment (16384 tokens, gates of -5 to -3:
+  // 0.00173 of dg, bf16's rounding alone 0.00167; three: 356 for 333 us of
   // gradients of 4 x 2048 tokens, 16 heads of 128 x 128).
   constexpr int TP = G32 || DT == DT_F16 ? 3 : 2;
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
@@ -1093,30 +1113,35 @@ __global__ __launch_bounds__(NW * 64, NV > 4 ? 1 : 2) void scan_grad_kernel(cons
     // from here on the next step may be staged: only the scores are still read,
     // and they are written again behind its own barrier
     __syncthreads();
+    f32x4 all_o[2][2];   // with a token's own term; o is without
 #pragma unroll
     for (int it = 0; it < 2; ++it) {
       bf16x8 ps[TP];
       get_scores<TP>(sc, it, lane, ps);
+      const bf16x8 p2[2] = {ps[0], ps[1]};
+      drop_own(ps, it, lane);
 #pragma unroll
       for (int nt = 0; nt < 2; ++nt) {
-        if constexpr (TP == 3) {
-          o[it][nt] = mfma_terms(ps, kk[nt], o[it][nt]);
-        } else {
-          const bf16x8 k2[2] = {kk[nt][0], kk[nt][1]};
-          o[it][nt] = mfma_terms(ps, k2, o[it][nt]);
-        }
+        const bf16x8 k2[2] = {kk[nt][0], kk[nt][1]};
+        all_o[it][nt] = mfma_terms(p2, k2, o[it][nt]);
+        if constexpr (TP == 3) o[it][nt] = mfma_terms(ps, kk[nt], o[it][nt]);
+        else o[it][nt] = mfma_terms(ps, k2, o[it][nt]);
       }
     }
     const __amdgpu_buffer_rsrc_t orsrc = chunk_rsrc(a.O, ob, nv);
     const Lane ot = fresh(ol);
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (now.width == 32 || takes(now, g, j))
+        store16<REV>(orsrc, ot, a.O.vec, j,
+                     pair_round<DT>(all_o[j >> 2][0][j & 3] * q.up[0][j] * a.oscale,
+                                    all_o[j >> 2][1][j & 3] * q.up[1][j] * a.oscale));
     float y[2][8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const float o0 = o[j >> 2][0][j & 3] * q.up[0][j] * a.oscale, o1 = o[j >> 2][1][j & 3] * q.up[1][j] * a.oscale;
       const bool mine = now.width == 32 || takes(now, g, j);
-      if (mine) store16<REV>(orsrc, ot, a.O.vec, j, pair_round<DT>(o0, o1));
-      y[0][j] = mine ? pair_lo<DT>(xw[j]) * o0 : 0.0f;
-      y[1][j] = mine ? pair_hi<DT>(xw[j]) * o1 : 0.0f;
+      y[0][j] = mine ? pair_lo<DT>(xw[j]) * (o[j >> 2][0][j & 3] * q.up[0][j] * a.oscale) : 0.0f;
+      y[1][j] = mine ? pair_hi<DT>(xw[j]) * (o[j >> 2][1][j & 3] * q.up[1][j] * a.oscale) : 0.0f;
     }
     // the workspace's rows of this chunk: the lane's tokens are rows of H dkp floats
     float* qr = qdq + tok * a.H * a.dkp + col;

@@ -26,10 +26,11 @@ slabs of 4 instructions and a tree of 16: 2 * 48 = 96) and the scale (2); where
 the state and the factors are held as two bf16 terms (four factors within 2^-17
 each) 2^-15, else 4 u.
 
-The gates' gradient runs from the end as sum of q dq - k dk, anchored at the
-ends of segments (multiples of 32 tokens) by sum(S D): the worst anchor, plus the
-errors of the later terms, plus 12 roundings a chunk of partial sums no larger
-than the sum of |terms|.
+The gates' gradient runs from the end as sum of q dq - k dk, without a token's own
+term in either (they are the same, and under strong gates all but a little of
+both), anchored at the ends of segments (multiples of 32 tokens) by sum(S D): the
+worst anchor, plus the errors of the later terms, plus 12 roundings a chunk of
+partial sums no larger than the sum of |terms|.
 """
 import numpy as np
 
@@ -98,7 +99,16 @@ def backward(q, k, v, g, do, scale, S0=None, dST=None, terms=2):
     rel = TWO_TERMS if terms == 2 else 4 * U
     n = ("dq", "dk", "dv", "dg")
     out, b = ({x: np.zeros(y.shape) for x, y in zip(n, (q, k, v, g))} for _ in range(2))
+    term, err = np.zeros(g.shape), np.zeros(g.shape)       # |q dq| + |k dk| without own terms, and its error
+    Cf, Cr = cost(g, k != 0), cost(g, q != 0)
     for i in range(t):
+        own_f = np.abs(k[i][:, :, None] * v[i][:, None, :])
+        own_r = np.abs(scale * q[i][:, :, None] * do[i][:, None, :])
+        for (s, a, e), own, C, x, y in ((f[i], own_f, Cf, do[i], abs(scale) * q[i]), (r[i], own_r, Cr, v[i], k[i])):
+            a, e = a - own, e - C[i // 32][:, :, None] * own
+            w = np.abs(x)[:, None, :]
+            term[i] += np.abs(y) * (w * a).sum(2)
+            err[i] += np.abs(y) * (w * (U * (e + 98 * a) + rel * a)).sum(2)
         s, a, e = f[i]
         out["dq"][i] = scale * (s * do[i][:, None, :]).sum(2)
         b["dq"][i] = abs(scale) * (np.abs(do[i])[:, None, :] * (U * (e + 98 * a) + rel * a)).sum(2)
@@ -125,8 +135,6 @@ def backward(q, k, v, g, do, scale, S0=None, dST=None, terms=2):
         size[i] = (a * x[0]).sum(2)
         anchor[i] = U * (er * x[0] + a * x[1] + 40 * a * x[0]).sum(2)
     ends = [i for i in range(t) if i % 32 == 31 or i == t - 1]
-    term = np.abs(q * out["dq"]) + np.abs(k * out["dk"])
-    err = np.abs(q) * b["dq"] + np.abs(k) * b["dk"]
     total = np.cumsum(term[::-1], 0)[::-1]
     later = np.cumsum(err[::-1], 0)[::-1]
     for i in range(t):

@@ -58,8 +58,16 @@ def check(x, o, ST, r, scale=None):
 
 # ---- the bounds themselves ------------------------------------------------------------
 
+# gates that chunks of 32 tokens, steps of 8 and steps of 1 take
+EVEN = {"even": (-2.4, -1.6), "even8": (-5.0, -3.0), "even1": (-10.0, -7.0)}
+
+
 def inputs(kind, t, dk, dv, dt, gt):
     x = tg.inputs(1, t, 2, dk, dv, dt, gt, gate=4.0)
+    if kind in EVEN:
+        lo, hi = EVEN[kind]
+        x["g"][:] = lo + (hi - lo) * torch.rand(x["g"].shape, generator=torch.Generator().manual_seed(t))
+        return x
     return lone(x) if kind == "lone" else tg.hard_gates(x, kind)
 
 
@@ -90,7 +98,7 @@ def test_bounds_tell_two_terms_from_three(t):
     assert (off(1) > bS).mean() > 0.5
 
 
-@pytest.mark.parametrize("kind", ["lone", "strong", "spikes", "reset", "growing"])
+@pytest.mark.parametrize("kind", ["lone", "strong", "spikes", "reset", "growing", *EVEN])
 @pytest.mark.parametrize("gt", [BF, F32], ids=["bf16", "f32gate"])
 def test_bounds_are_narrow_and_agree_with_the_reference(kind, gt):
     """The references give the same values, and float32 results are held to 2^-14 of their
@@ -111,7 +119,7 @@ def test_bounds_are_narrow_and_agree_with_the_reference(kind, gt):
 # ---- the kernels ------------------------------------------------------------------------
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("kind", ["lone", "strong", "spikes", "reset", "growing"])
+@pytest.mark.parametrize("kind", ["lone", "strong", "spikes", "reset", "growing", *EVEN])
 @pytest.mark.parametrize("t,dk,dv", [(32, 64, 64), (70, 64, 64), (130, 128, 96), (300, 40, 256)])
 @pytest.mark.parametrize("dt,gt", tg.TYPES, ids=tg.TIDS)
 def test_within_bounds(scan, kind, t, dk, dv, dt, gt):  # noqa: F811

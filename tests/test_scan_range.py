@@ -1,8 +1,10 @@
 """GPU: the GLA scan where decays, states or values are far apart in size,
 within the bounds of scan_bounds."""
+import numpy as np
 import pytest
 import torch
 
+import scan_ref
 import test_gla_scan as tg
 from test_gla_scan import scan  # noqa: F401 (fixture)
 from test_scan_bounds import check
@@ -128,3 +130,22 @@ def test_gate_gradient_before_a_reset(scan, dt, gt, heads):  # noqa: F811
     rows = {n: y[:, :150] if n != "dS0" else y for n, y in r.items()}
     assert (r["dg"][:, 150] == 0).all()
     check(first, o[:, :150], None, rows)
+
+
+@pytest.mark.parametrize("lo,hi", [(-5.0, -3.0), (-10.0, -7.0)])
+@pytest.mark.parametrize("dt,gt", tg.TYPES, ids=tg.TIDS)
+def test_gate_gradient_under_strong_gates(scan, dt, gt, lo, hi):  # noqa: F811
+    """A whole sequence of 2048 tokens whose dg is e^g of a token's own q dq and k dk.  dg is a running
+    sum of 2 t terms from pairs of different tokens, each about as large as dg (nearly all from
+    neighbours, e^-3 at the least of what comes from further); a product in them is within 2^-15 (two
+    bf16 terms in four factors) or 100 u (three, fp32 sums), independently of the others: sqrt(2 t)
+    times that, beside the result's own rounding."""
+    t = 2048
+    x = tg.inputs(1, t, 1, 32, 32, dt, gt, state=False)
+    x["g"][:] = lo + (hi - lo) * torch.rand(x["g"].shape, generator=torch.Generator().manual_seed(1))
+    _, _, r = run(scan, x, 1024)
+    want, _ = scan_ref.backward(*[tg.f64(x[n][0]) for n in ("q", "k", "v", "g", "do")], x["scale"])
+    each = 2.0 ** -15 if dt == BF and gt == BF else 100 * scan_ref.U
+    f = torch.finfo(gt)
+    tol = (each * (2 * t) ** 0.5 + f.eps / 2) * np.linalg.norm(want["dg"]) + f.smallest_normal * f.eps / 2 * want["dg"].size ** 0.5
+    assert np.linalg.norm(r["dg"][0].double().cpu().numpy() - want["dg"]) <= tol
