@@ -1268,11 +1268,10 @@ __global__ __launch_bounds__(NW * 64, NV > 4 ? 1 : 2) void scan_grad_kernel(cons
 // the recurrence, so a token's factor is the running product of what has been
 // walked and the sums are never rescaled: no chunk is cut for its gates' sake,
 // and a factor that underflows belongs to a contribution that has decayed.
-// Where that does not hold -- factors or values beyond kBig, factors that
-// rise again after they were tiny, 8 gates whose product is not a normal number
-// -- the wave does its channels over again as the recurrence itself.  The
-// segment's whole decay, for the state at its start, is kept with an exponent of
-// its own.  K and its factors stay in a wave's registers, V is
+// Where that does not hold -- factors or values beyond kBig, or factors that
+// rise again after they were tiny -- the wave does its channels over again as
+// the recurrence itself.  The segment's whole decay, for the state at its start,
+// is kept with an exponent of its own.  K and its factors stay in a wave's registers, V is
 // shared through LDS in two buffers of its terms (f16 is converted once a
 // workgroup: 73 us for 83 at 32768 tokens, 8 heads), one barrier a chunk.  Bound
 // by HBM: at the sizes above 27 us (88 MB read, 29 MB written: 4.3 TB/s; further
@@ -1346,20 +1345,22 @@ __device__ __forceinline__ void own_state(const ScanArgs& a) {
     float top = 0.0f;
 #pragma unroll
     for (int ch = 0; ch < 2; ++ch) {
-      float P[8], of = 1.0f, bottom = 0.0f;
+      float P[8], of = 1.0f;
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const float x = gate_value<DT, G32>(gw, ch, j);
         top = __builtin_fmaxf(top, x);
-        bottom = __builtin_fminf(bottom, x);
         const float e = __builtin_amdgcn_exp2f(x * 1.44269504f);
         if (DIR) P[j] = of;
         of = j == 0 ? e : of * e;
         if (!DIR) P[j] = of;
       }
-      times(whole[ch], of);
-      // a gate of -104 is a factor of 0 in float32
-      if (of < 0x1p-120f && bottom > -104.0f) big = __builtin_inff();
+      if (of >= 0x1p-120f) {
+        times(whole[ch], of);
+      } else {   // (or NaN) the product has lost bits, the factors have not
+#pragma unroll
+        for (int j = 0; j < 8; ++j) times(whole[ch], expf(gate_value<DT, G32>(gw, ch, j)));
+      }
       // times the groups walked before this one, and the chunks before
       const float next = __shfl_xor(of, 16, 64), both = of * next;
       const float other = __shfl_xor(both, 32, 64);
