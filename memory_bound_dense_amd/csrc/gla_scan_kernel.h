@@ -433,33 +433,34 @@ constexpr int kTokRow = kScanC + 8;     // tokens per row of a transposed tile, 
 // the gates or values do not allow it, 8 (those of one lane group) or 1.  A step
 // scales the state by its own first half's decay and what the step before left, in
 // one product; of a token's decay, which may be anything, that product could leave
-// float32's range where the state does not.  So a step of no tokens (its `then`
-// is the width behind it) lies between steps of one token, whose decay is the first
-// half forward and what is left reversed, and those with another half of theirs there.
+// float32's range where the state does not.  A step of one token has all its decay
+// before it (forward) or leaves all of it (reversed); where its neighbour there has
+// another half of its own, a step of no tokens goes between them.
+// `then` of a step of several tokens is the width of the step to be taken first if it
+// is refused (forward), or whether a token's decay is left for it (reversed); of a
+// step of none the width behind it.
 struct Step {
   int pos, width, then;
 };
 __device__ __forceinline__ bool takes(const Step& t, int g, int j) {
   return (uint32_t)(8 * g + j - t.pos) < (uint32_t)t.width;
 }
-// What a step that was refused is tried with, the step after `t`, and the next
-// chunk's first one.
+// What is taken instead of a step of several tokens, the step after `t`, and the
+// next chunk's first one.
 template <bool REV>
-__device__ __forceinline__ void smaller(Step& t) {
-  if (t.width == 32) t.width = 8;
-  else if (REV) t.width = 1;
-  else t = Step{t.pos, 0, 1};
+__device__ __forceinline__ void smaller(Step& t, bool refused) {
+  if (REV && !refused) t = Step{t.pos, 0, t.width};
+  else if (t.width == 32) t.width = 8;
+  else t = REV ? Step{t.pos, 1, 0} : Step{t.pos, t.then, 1};
 }
 template <bool REV>
 __device__ __forceinline__ void advance(Step& t) {
   t.pos += t.width;
-  if (t.width == 0) t.width = t.then;
-  else if ((t.pos & 7) == 0 && t.width == 1) t = REV ? Step{t.pos, 0, 8} : Step{t.pos, 8, 0};
+  if (t.width == 0) t = Step{t.pos, t.then, 0};
+  else if ((t.pos & 7) == 0 && t.width == 1) t = Step{t.pos, 8, 1};
+  else t.then = 0;
 }
-template <bool REV>
-__device__ __forceinline__ Step first_step(const Step& before) {
-  return REV && before.width == 1 ? Step{0, 0, 32} : Step{0, 32, 0};
-}
+__device__ __forceinline__ Step first_step(const Step& before) { return Step{0, 32, before.width == 1 ? 1 : 0}; }
 // The words of the step's tokens; others read as 0.
 __device__ __forceinline__ void take(const Step& t, int g, const uint32_t (&from)[8], uint32_t (&to)[8]) {
 #pragma unroll
@@ -667,7 +668,7 @@ __global__ __launch_bounds__(NW * 64, NS > 4 ? 1 : 2) void scan_out_kernel(const
   float left[SL][2], half[SL][2];
 #pragma unroll
   for (int i = 0; i < SL; ++i) left[i][0] = left[i][1] = half[i][0] = half[i][1] = 1.0f;
-  Step st = {0, 32, 0};
+  Step st = {0, 32, REV ? 0 : 1};
   for (int c = 0; c < nch;) {
     const int64_t tok = p.lo + (int64_t)(REV ? nch - 1 - c : c) * kScanC;
     const int nv = (int)min((int64_t)kScanC, p.hi - tok);
@@ -728,8 +729,9 @@ __global__ __launch_bounds__(NW * 64, NS > 4 ? 1 : 2) void scan_out_kernel(const
     int all = 0;
 #pragma unroll
     for (int w = 0; w < NW; ++w) all |= wild[w];
-    if (st.width > 1 && __builtin_amdgcn_readfirstlane(all)) {
-      smaller<REV>(st);
+    all = __builtin_amdgcn_readfirstlane(all);
+    if (st.width > 1 && (all | (REV ? st.then : 0))) {
+      smaller<REV>(st, all != 0);
       __syncthreads();
       continue;
     }
@@ -745,7 +747,7 @@ __global__ __launch_bounds__(NW * 64, NS > 4 ? 1 : 2) void scan_out_kernel(const
     advance<REV>(st);
     const int next = st.pos == kScanC ? c + 1 : c;
     if (next != c) {
-      st = first_step<REV>(now);
+      st = first_step(now);
       if (next < nch) fetch(next);   // in flight during the products
     }
     f32x4 o[2][2] = {};
@@ -968,7 +970,7 @@ __global__ __launch_bounds__(NW * 64, NV > 4 ? 1 : 2) void scan_grad_kernel(cons
   if (nch > 0) fetch(0);
   if (!REV) load_state();
   float left[2] = {1.0f, 1.0f};   // a step's second half e^{end-r}, done with the next step's first
-  Step st = {0, 32, 0};
+  Step st = {0, 32, REV ? 0 : 1};
   for (int c = 0; c < nch;) {
     const int64_t tok = p.lo + (int64_t)(REV ? nch - 1 - c : c) * kScanC;
     const int nv = (int)min((int64_t)kScanC, p.hi - tok);
@@ -1036,8 +1038,9 @@ __global__ __launch_bounds__(NW * 64, NV > 4 ? 1 : 2) void scan_grad_kernel(cons
     int all = 0;
 #pragma unroll
     for (int w = 0; w < NW; ++w) all |= wild[w];
-    if (st.width > 1 && __builtin_amdgcn_readfirstlane(all)) {
-      smaller<REV>(st);
+    all = __builtin_amdgcn_readfirstlane(all);
+    if (st.width > 1 && (all | (REV ? st.then : 0))) {
+      smaller<REV>(st, all != 0);
       __syncthreads();
       continue;
     }
@@ -1053,7 +1056,7 @@ __global__ __launch_bounds__(NW * 64, NV > 4 ? 1 : 2) void scan_grad_kernel(cons
     advance<REV>(st);
     const int next = st.pos == kScanC ? c + 1 : c;
     if (next != c) {
-      st = first_step<REV>(now);
+      st = first_step(now);
       if (next < nch) fetch(next);   // in flight during the products
     }
     f32x4 o[2][2] = {};
