@@ -13,7 +13,7 @@ namespace mbd {
 // slots[s] holds segment s's own state (from zero; the last segment's in the
 // order of the recurrence is not there, and not needed) and becomes its start
 // state: one thread per 4 elements walks the sequence's segments.  Bound by HBM
-// (64 heads of 128 x 128, 8 segments: 63 MB in 10.4 us, 6.0 TB/s) and, for few
+// (64 heads of 128 x 128, 8 segments: 63 MB in 10.6 us, 5.9 TB/s) and, for few
 // heads, by the walk (15 heads of 64 x 96, 32 segments, both sides: 12 us, 15 with
 // 4 segments fetched at once).
 struct Join {

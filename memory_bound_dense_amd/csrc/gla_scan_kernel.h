@@ -863,9 +863,11 @@ __global__ __launch_bounds__(NW * 64, NS > 4 ? 1 : 2) void scan_out_kernel(const
 // A wave owns 32 channels (columns of the transposed state, 64 VGPRs at DV
 // 128) and their part of the output; K e^{r-G} of its channels never leaves
 // its registers.  V and W go through LDS, row-major for the products over DV
-// and V also transposed for the state's update.  At the sizes above: dq 89 us
-// with q dq left in float32 for the gates' gradient (235 MB: 2.6 TB/s), dk with
-// dg 102 us (270 MB), bound as above.
+// and V also transposed for the state's update.  At the sizes above: dq 88 us
+// with q dq left in float32 for the gates' gradient (235 MB: 2.7 TB/s), dk with
+// dg 101 us (270 MB), bound as above, and by registers: 10 and 15 a lane are spilled
+// in bf16 at four waves of 128 columns, 20..40 with fp16 or float32 gates or two waves
+// (the 64-column forms none).
 
 template <int DT, int NV>
 constexpr size_t scan_grad_lds() {
