@@ -23,9 +23,10 @@
  * y / (1 + e^-y).
  *
  * Layout: row-major with leading dimensions lda, ldb >= k, ldc, ldr >= n, in
- * elements (that of a single row is not used, nor limited below); every tensor needs the alignment of its element only (16-byte
- * aligned rows are faster).  C must not overlap anything else, except that
- * residual may be C itself with ldr == ldc.
+ * elements (that of a single row is not used, nor limited below); every tensor
+ * needs the alignment of its element only (16-byte aligned rows are faster).  C
+ * must not overlap anything else, except that residual may be C itself with
+ * ldr == ldc.
  *
  * Like gemv_run: host validation, kernels enqueued on `stream`, no allocation,
  * no synchronisation; on any error nothing is launched.  m == 0 or n == 0 is a

@@ -17,15 +17,15 @@
  * are float32, dense (sequence, head, dk, dv), the layout of gla_decode_step.
  * States and all sums are held in float32; each 16-bit output is rounded once,
  * to nearest-even.  Decayed q, k and dout, scores and states enter the products
- * with 16 bits (within 2^-17) where the result is rounded to 16 bits, with 24 where it
- * goes into a state or the gates' gradient, which is a running sum over the
- * tokens (bf16 gates of bf16 tensors: 16 bits, half a bf16 step after some 10^5
- * tokens).  Any gate is taken: one of -inf clears the state, positive
- * ones let it grow; a token's exp(gk) is a float32 (0 below -104, infinite
- * above 88.7), as in gla_decode_step, the decay over many tokens is not.  A
- * value that is not finite reaches the outputs that depend on it and no earlier
- * token's (o) or later token's (gradients of k and v); a state that holds one
- * makes every output that reads its row NaN or infinite.
+ * with 16 bits (within 2^-17) where the result is rounded to 16 bits, with 24
+ * where it goes into a state or the gates' gradient, which is a running sum over
+ * the tokens (bf16 gates of bf16 tensors: 16 bits, half a bf16 step after some
+ * 10^5 tokens).  Any gate is taken: one of -inf clears the state, positive ones
+ * let it grow; a token's exp(gk) is a float32 (0 below -104, infinite above
+ * 88.7), as in gla_decode_step, the decay over many tokens is not.  A value that
+ * is not finite reaches the outputs that depend on it and no earlier token's (o)
+ * or later token's (gradients of k and v); a state that holds one makes every
+ * output that reads its row NaN or infinite.
  *
  * Layout: element strides per tensor, so (batch, token, head, channel) and
  * (batch, head, token, channel) tensors and slices of fused projections are

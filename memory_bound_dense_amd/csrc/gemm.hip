@@ -18,8 +18,8 @@ using GemmFn = void (*)(const mbd::GemmArgs);
 
 // Tiles: rows of B x tokens, and what a slab costs, in ns: `alone` for one
 // workgroup on a CU, `shared` per workgroup where the CU has more to do.
-// Measured (bf16, and used for every type): the tile's time over whole rounds, e.g. aligned 256 x 256
-// 94 us for 64 slabs on 86 CUs and 98 us on 256; 128 x 128 52 us for 64 slabs
+// Measured (bf16, and used for every type): the tile's time over whole rounds,
+// e.g. aligned 256 x 256 94 us for 64 slabs on 86 CUs and 98 us on 256; 128 x 128 52 us for 64 slabs
 // on 256 CUs, 116 us for 4 workgroups a CU; 64 x 64 30 us for 64 slabs, 190 us
 // for 16 a CU.
 struct Tile {

@@ -32,7 +32,8 @@
 // every fp32 factor enters as a sum of bf16 terms -- two (2^-17 relative) where
 // the result is rounded to 16 bits right after, three (2^-25) where it goes
 // into the fp32 state or the gradient of the gates, which is a running sum (two
-// there too if it and the tensors are bf16: see scan_grad_kernel).  q, k, v and do are exact in one term (bf16) or two (f16).
+// there too if it and the tensors are bf16: see scan_grad_kernel).  q, k, v and do
+// are exact in one term (bf16) or two (f16).
 //
 // Layout.  16x16x32 matrix instructions: an operand's lane (n = lane & 15,
 // g = lane >> 4) holds row/column n and the 8 depth positions 8g..8g+7; a
