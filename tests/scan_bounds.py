@@ -10,6 +10,8 @@ it is born and in every later one, the chunk's cost
 
   * c(g): a gate's factor.  0 is the exact factor 1.  |g| > 40 is applied by
     itself: its exponential is within one unit (2 u), its product rounds once: 3.
+    (Below 2^-126 the exponential is a multiple of 2^-149, or 0 and off by all of
+    it: what decays by it is charged that.)
     Others: x log2(e) is rounded (u |x|, in the result) and the constant is off by
     0.23 u: 1.3 |g|; the exponential 2, its product with the others 1.  Twice,
     since a pair's decay is a ratio of two products of the chunk.
@@ -54,8 +56,8 @@ def cost(g, births):
 
 
 def _walk(k, v, g, S0, dv, reverse):
-    """Per token the state after it (forward) or before its gate (reversed) and its
-    A and E; then the last state's.  k already scaled."""
+    """Per token the state after it (forward) or before its gate (reversed), its A and E, and
+    A and E without the token's own term; then the last state's.  k already scaled."""
     t, h, dk = k.shape
     C = cost(g, k != 0)
     S = np.zeros((h, dk, dv)) if S0 is None else S0.astype(np.float64).copy()
@@ -67,15 +69,17 @@ def _walk(k, v, g, S0, dv, reverse):
         if i == (min(t, (i // 32 + 1) * 32) - 1 if reverse else i // 32 * 32):
             E = E + c * A
         e = np.exp(g[i])[:, :, None]
+        low = np.where(g[i][:, :, None] < -87, np.minimum(e, 2.0 ** -149) / U, 0.0)
         new = k[i][:, :, None] * v[i][:, None, :]
         if not reverse:
-            S, A, E = e * S, e * A, e * E
+            S, A, E = e * S, e * A, e * E + low * A
+        others = A, E
         S = S + new
         A = A + np.abs(new)
         E = E + c * np.abs(new)
-        hist[i] = (S, A, E)
+        hist[i] = (S, A, E) + others
         if reverse:
-            S, A, E = e * S, e * A, e * E
+            S, A, E = e * S, e * A, e * E + low * A
     return hist, (S, A, E)
 
 
@@ -83,7 +87,7 @@ def forward(q, k, v, g, scale, S0=None):
     """o, ST and the bounds of their errors before the outputs' rounding."""
     hist, (S, A, E) = _walk(k, v, g, S0, v.shape[2], False)
     o, b = np.zeros(v.shape), np.zeros(v.shape)
-    for i, (s, a, e) in enumerate(hist):
+    for i, (s, a, e, _, _) in enumerate(hist):
         o[i] = scale * (q[i][:, :, None] * s).sum(1)
         b[i] = abs(scale) * (np.abs(q[i])[:, :, None] * (U * (e + 98 * a) + TWO_TERMS * a)).sum(1)
     return o, S, b, U * E + U * np.abs(S)
@@ -100,19 +104,15 @@ def backward(q, k, v, g, do, scale, S0=None, dST=None, terms=2):
     n = ("dq", "dk", "dv", "dg")
     out, b = ({x: np.zeros(y.shape) for x, y in zip(n, (q, k, v, g))} for _ in range(2))
     term, err = np.zeros(g.shape), np.zeros(g.shape)       # |q dq| + |k dk| without own terms, and its error
-    Cf, Cr = cost(g, k != 0), cost(g, q != 0)
     for i in range(t):
-        own_f = np.abs(k[i][:, :, None] * v[i][:, None, :])
-        own_r = np.abs(scale * q[i][:, :, None] * do[i][:, None, :])
-        for (s, a, e), own, C, x, y in ((f[i], own_f, Cf, do[i], abs(scale) * q[i]), (r[i], own_r, Cr, v[i], k[i])):
-            a, e = a - own, e - C[i // 32][:, :, None] * own
+        for (_, _, _, a, e), x, y in ((f[i], do[i], abs(scale) * q[i]), (r[i], v[i], k[i])):
             w = np.abs(x)[:, None, :]
             term[i] += np.abs(y) * (w * a).sum(2)
             err[i] += np.abs(y) * (w * (U * (e + 98 * a) + rel * a)).sum(2)
-        s, a, e = f[i]
+        s, a, e = f[i][:3]
         out["dq"][i] = scale * (s * do[i][:, None, :]).sum(2)
         b["dq"][i] = abs(scale) * (np.abs(do[i])[:, None, :] * (U * (e + 98 * a) + rel * a)).sum(2)
-        s, a, e = r[i]
+        s, a, e = r[i][:3]
         out["dk"][i] = (s * v[i][:, None, :]).sum(2)
         b["dk"][i] = (np.abs(v[i])[:, None, :] * (U * (e + 98 * a) + rel * a)).sum(2)
         out["dv"][i] = (s * k[i][:, :, None]).sum(1)
@@ -124,7 +124,7 @@ def backward(q, k, v, g, do, scale, S0=None, dST=None, terms=2):
         e = np.exp(g[i])[:, :, None]
         before = f[i - 1] if i else ((np.zeros((h, dk, dv)),) * 3 if S0 is None else (S0, np.abs(S0), 0 * S0))
         out["dg"][i] = (e * before[0] * r[i][0]).sum(2)
-        s, a, er = f[i]
+        s, a, er = f[i][:3]
         if i + 1 < t:
             e = np.exp(g[i + 1])[:, :, None]
             x = (e * r[i + 1][1], e * r[i + 1][2])

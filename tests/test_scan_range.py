@@ -1,5 +1,7 @@
 """GPU: the GLA scan where decays, states or values are far apart in size,
 within the bounds of scan_bounds."""
+import random
+
 import numpy as np
 import pytest
 import torch
@@ -149,3 +151,24 @@ def test_gate_gradient_under_strong_gates(scan, dt, gt, lo, hi):  # noqa: F811
     f = torch.finfo(gt)
     tol = (each * (2 * t) ** 0.5 + f.eps / 2) * np.linalg.norm(want["dg"]) + f.smallest_normal * f.eps / 2 * want["dg"].size ** 0.5
     assert np.linalg.norm(r["dg"][0].double().cpu().numpy() - want["dg"]) <= tol
+
+
+@pytest.mark.parametrize("seed", range(24))
+def test_random_sizes_and_gates(scan, seed):  # noqa: F811
+    """Sizes, head counts (so segments) and mixtures of gates at random: none, mild, strong, single
+    ones and whole tokens of -inf, positive ones, channels that always forget."""
+    rng = random.Random(seed)
+    t, dk, dv = int(400 ** rng.random()), rng.choice([1, 7, 16, 33, 64, 100]), rng.choice([1, 8, 15, 40, 64, 130])
+    dt, gt = rng.choice(tg.TYPES)
+    x = tg.inputs(1, t, 1, dk, dv, dt, gt, gate=rng.choice([1.0, 4.0, 16.0]), seed=seed, state=rng.random() < 0.7)
+    gen = torch.Generator().manual_seed(seed)
+    g = x["g"].float()
+    for _ in range(rng.randint(1, 4)):
+        r = torch.rand(g.shape, generator=gen)
+        to = rng.choice([0 * r, -1 - 4 * r, -5 - 10 * r, -20 - 55 * r, 0 * r - float("inf"), 0.3 * r])
+        shape = rng.choice([g.shape, (1, t, 1, 1), (1, 1, 1, dk)])
+        g = torch.where((torch.rand(shape, generator=gen) < rng.choice([0.02, 0.2, 0.5])).expand_as(g), to, g)
+    # a state may grow by e^4 at most: its sum of positive gates is scaled to that
+    up = g.clamp(min=0).sum(1, keepdim=True)
+    x["g"] = torch.where(g > 0, g * (4 / up.clamp(min=4)), g).to(gt)
+    check(x, *run(scan, x, rng.choice([1, 3, 40, 300])))
